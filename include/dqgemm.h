@@ -239,6 +239,57 @@ dqgemm_status dqgemm_quantize_act_fp8(const void* x, int M, int K, float s_x,
 dqgemm_status dqgemm_quantize_act_fp4(dqgemm_format fmt, const void* x, int M, int K,
                                       void* codes, void* scales, float* g_x, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Row operators of a feed-forward block: the steps between the products, with
+ * their output already in 8 bits.  x: device [M, K] of `type`, rows `ldx`
+ * elements apart (ldx >= K; a column slice of a wider tensor is fine), every
+ * other tensor dense.  Arithmetic is fp32; each output carries one rounding.
+ * `out_kind`:
+ *   DQ_OUT_BF16, _FP16, _FP32   out [M, K] of that type
+ *   DQ_OUT_FP8_BLOCK            out u8 [M, K] e4m3 codes, scales fp32
+ *       [M, ceil(K / 128)]: s = f32(amax / 448) over 128 consecutive elements
+ *       of a row (the last block may be shorter), code = e4m3(f32(v / s)),
+ *       round to nearest even.  s = 0 (a zero block, or one whose amax / 448
+ *       underflows) gives codes 0; a NaN makes its block's scale and codes
+ *       NaN; an infinity makes the scale infinite, its own code NaN and the
+ *       block's other codes 0.
+ *   DQ_OUT_FP8_STATIC           out u8 [M, K]: e4m3(f32(v / s_out)),
+ *       saturating, the codes that a DQ_FP8_STATIC layer calibrated with
+ *       s_out takes (dqgemm_run_fp8_static_quantized); s_out finite and > 0
+ * Buffers need their natural alignment only; 16-byte aligned rows (8-byte
+ * for codes) are moved in vectors, others element by element.
+ * M >= 1, 1 <= K <= 2^28.  One launch on `stream`, no allocation, no
+ * synchronization; programmatic dependent launch as dqgemm_run, and nothing
+ * is read or written before the previous kernel of the stream has completed. */
+typedef enum { DQ_BF16 = 0, DQ_FP16 = 1, DQ_FP32 = 2 } dqgemm_dtype;
+typedef enum {
+  DQ_OUT_BF16 = 0,
+  DQ_OUT_FP16 = 1,
+  DQ_OUT_FP32 = 2,
+  DQ_OUT_FP8_BLOCK = 3,
+  DQ_OUT_FP8_STATIC = 4
+} dqgemm_out;
+
+/* Root-mean-square norm with the residual's addition:
+ *     r = x + residual,   v[m, k] = r[m, k] * w[k] / sqrt(mean_k r^2 + eps)
+ * `residual` and `residual_out` ([M, K] of `type`) are both given or both
+ * NULL; residual_out receives r rounded to `type`, and may be `residual` or
+ * x (with ldx == K) itself.  The norm is of the unrounded sum.  `weight`: [K]
+ * of weight_type, or NULL for ones.  eps >= 0.  A row is read once up to
+ * K = 16384, twice beyond. */
+dqgemm_status dqgemm_rmsnorm(dqgemm_dtype type, const void* x, long long ldx, const void* residual,
+                             void* residual_out, dqgemm_dtype weight_type, const void* weight, float eps, int M, int K,
+                             dqgemm_out out_kind, float s_out, void* out, float* scales, void* stream);
+
+/* Gated SiLU: x [M, 2K] holds the gate g in its first K columns and u in the
+ * others (ldx >= 2K);  v = g / (1 + exp(-g)) * u. */
+dqgemm_status dqgemm_silu_mul(dqgemm_dtype type, const void* x, long long ldx, int M, int K, dqgemm_out out_kind,
+                              float s_out, void* out, float* scales, void* stream);
+
+/* Activation quantization with a scale per 128: v = x, DQ_OUT_FP8_BLOCK. */
+dqgemm_status dqgemm_quantize_act_fp8_block(dqgemm_dtype type, const void* x, long long ldx, int M, int K, void* q,
+                                            float* scales, void* stream);
+
 /* Quantize and pack a host fp32 weight [N, K] into the canonical layout of
  * `fmt` (host outputs `packed` and `scales`, sized as listed above).  The
  * recipes (fp32 operations, round to nearest even):

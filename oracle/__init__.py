@@ -13,9 +13,11 @@ quant     the weight quantizers and the nibble packer of the five formats.
 linear    dequantization, the fp64 GEMM reference, static-FP8 activation
           quantization and calibration, SQNR, and the FP4 x FP4 reference
           (dynamic MX / NVFP4 activation quantization).
+block     the block-scaled FP8 operators: row norm, gated SiLU, quantizers and
+          products (dense, and by expert).
 
 Parity status of every function is stated in its docstring; functions whose
 result is not pinned by an independent check say "parity unpinned".
 """
 
-from . import formats, quant, linear  # noqa: F401
+from . import block, formats, quant, linear  # noqa: F401

@@ -1,0 +1,237 @@
+"""The row operators (RMS norm with residual, gated SiLU, block-scaled FP8
+quantizer) against the fp64 oracle.
+
+Tolerances.  u = 2^-24 is half a step of fp32.  A row's sum of squares takes at
+most K / 4096 + 7 fused multiply-adds in turn per element slot of a thread (8
+of them a vector) and 9 additions across threads, each within u of its value,
+so its square root is within (8 (K / 4096 + 1) + 9) / 2 + 1 of u; the residual's
+sum, the reciprocal root (2 units of 2^-23), and two products add 8 u.  The
+gated SiLU's hardware exponential is within 2 + 1.16 |g| units of 2^-23 and its
+division within 2.  Every output then carries half a step of its type, with an
+absolute part below the type's smallest normal; for a code the half step is
+2^-4 of the value, or 2^-10 scales below 2^-6 scales."""
+
+import numpy as np
+import pytest
+import torch
+
+import weight_only_quantized_prologue_b200 as dq
+from oracle import block as B
+from oracle import formats as F
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -24}
+TINY = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25, "fp32": 2.0 ** -150}   # half the subnormal spacing
+
+
+def gen(shape, seed, dt, scale=1.0):
+    g = torch.Generator("cpu").manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(DT[dt]).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def norm_rel(K):
+    return ((8 * (K / 4096 + 1) + 9) / 2 + 9) * U
+
+
+def check_float(y, ref, dt, rel):
+    bound = np.abs(ref) * (rel + HALF[dt]) + TINY[dt] + 2.0 ** -149
+    bad = ~(np.abs(f64(y) - ref) <= bound)
+    assert not bad.any(), (bad.sum(), np.abs(f64(y) - ref).max())
+
+
+def check_codes(q, s, ref, rel):
+    """Codes and scales against the unquantized fp64 values, each within rel."""
+    q, s = q.cpu().numpy(), s.cpu().numpy()
+    M, K = ref.shape
+    pad = np.zeros((M, s.shape[1] * 128))
+    pad[:, :K] = np.abs(ref)
+    amax = pad.reshape(M, -1, 128).max(2)
+    sw = s.astype(np.float64)
+    assert (np.abs(sw - amax / 448) <= amax / 448 * (rel + 2 * U) + 2.0 ** -149).all()
+    wide = np.repeat(sw, 128, 1)[:, :K]
+    got = F.e4m3_decode(q) * wide
+    bound = np.maximum(np.abs(ref) * 2.0 ** -4, wide * 2.0 ** -10) * 1.0001 + np.abs(ref) * (2 * rel + 4 * U) + 2.0 ** -148
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), bad.sum()
+
+
+SIZES = [(1, 1), (3, 7), (2, 8), (5, 120), (1, 128), (4, 136), (9, 257), (130, 1000), (17, 2048), (33, 4096),
+         (7, 5008), (2, 8200), (3, 16384), (2, 20008), (1, 40001)]
+
+
+@pytest.mark.parametrize("M,K", SIZES)
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_quantizer_is_bit_exact(M, K, dt):
+    x = gen((M, K), 1, dt, 3.0)
+    q, s = dq.quantize_act_fp8_block(x)
+    rq, rs = B.quantize_rows(f64(x))
+    assert np.array_equal(s.cpu().numpy().view(np.uint32), rs.view(np.uint32))
+    assert np.array_equal(q.cpu().numpy(), rq)
+
+
+@pytest.mark.parametrize("M,K", SIZES)
+@pytest.mark.parametrize("dt,odt", [("bf16", None), ("fp16", None), ("fp32", None), ("fp32", "bf16"), ("bf16", "fp32")])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm_float_outputs(M, K, dt, odt, residual):
+    x, w = gen((M, K), 2, dt, 2.0), gen((K,), 3, dt)
+    r = gen((M, K), 4, dt, 2.0) if residual else None
+    got = dq.rmsnorm(x, w, 1e-5, residual=r, out_dtype=None if odt is None else DT[odt])
+    ref, rsum = B.rmsnorm(f64(x), f64(w), 1e-5, None if r is None else f64(r))
+    y = got[0] if residual else got
+    assert y.dtype == DT[odt or dt]
+    check_float(y, ref, odt or dt, norm_rel(K))
+    if residual:
+        check_float(got[1], rsum, dt, U)
+
+
+@pytest.mark.parametrize("M,K", SIZES)
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_rmsnorm_block_codes(M, K, dt):
+    x, w, r = gen((M, K), 5, dt), gen((K,), 6, dt), gen((M, K), 7, dt)
+    q, s, r2 = dq.rmsnorm(x, w, residual=r, quant="fp8_block")
+    ref, rsum = B.rmsnorm(f64(x), f64(w), 1e-6, f64(r))
+    check_codes(q, s, ref, norm_rel(K))
+    check_float(r2, rsum, dt, U)
+    # the codes are those of the fp32 norm
+    y, _ = dq.rmsnorm(x, w, residual=r, out_dtype=torch.float32)
+    q2, s2 = dq.quantize_act_fp8_block(y)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("wdt", ["bf16", "fp16", "fp32", None])
+def test_rmsnorm_weight_types_and_static_codes(wdt):
+    M, K = 19, 1048
+    x = gen((M, K), 8, "bf16")
+    w = None if wdt is None else gen((K,), 9, wdt)
+    s_out = 0.0123
+    q = dq.rmsnorm(x, w, quant="fp8_static", s_out=s_out)
+    y = dq.rmsnorm(x, w, out_dtype=torch.float32)
+    t = (f64(y) / np.float64(np.float32(s_out))).astype(np.float32).astype(np.float64)
+    assert np.array_equal(q.cpu().numpy(), F.e4m3_encode(F.e4m3_round(t)))
+
+
+@pytest.mark.parametrize("M,K", SIZES)
+@pytest.mark.parametrize("dt,odt", [("bf16", None), ("fp16", None), ("fp32", None), ("bf16", "fp32")])
+def test_silu_mul_float_outputs(M, K, dt, odt):
+    x = gen((M, 2 * K), 10, dt, 2.0)
+    y = dq.silu_mul(x, out_dtype=None if odt is None else DT[odt])
+    g = np.abs(f64(x)[:, :K])
+    check_float(y, B.silu_mul(f64(x)), odt or dt, (8 + 1.2 * g) * 2.0 ** -23)
+
+
+@pytest.mark.parametrize("M,K", SIZES)
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_silu_mul_codes(M, K, dt):
+    x = gen((M, 2 * K), 11, dt, 2.0)
+    ref = B.silu_mul(f64(x))
+    rel = float((8 + 1.2 * np.abs(f64(x)[:, :K]).max()) * 2.0 ** -23)
+    q, s = dq.silu_mul(x, quant="fp8_block")
+    check_codes(q, s, ref, rel)
+    s_out = 0.031
+    got = F.e4m3_decode(dq.silu_mul(x, quant="fp8_static", s_out=s_out).cpu().numpy()) * np.float64(np.float32(s_out))
+    want = np.clip(ref, -448 * s_out, 448 * s_out)
+    bound = np.maximum(np.abs(want) * 2.0 ** -4, s_out * 2.0 ** -10) * 1.0001 + np.abs(want) * (2 * rel + 4 * U)
+    assert (np.abs(got - want) <= bound).all()
+
+
+def test_silu_mul_at_the_ends_of_the_exponential():
+    # e^-g overflows below -88: the result tends to 0 with g's sign; large g gives g * u
+    g = torch.tensor([[-1e4, -120.0, -89.0, -0.0, 0.0, 89.0, 1e4, 3e38]])
+    x = torch.cat([g, torch.full_like(g, 2.0)], 1).cuda()
+    for dt in (torch.float32, torch.bfloat16):
+        y = dq.silu_mul(x, out_dtype=dt)[0].float().cpu()
+        assert (y[:3].abs() < 1e-30).all() and (y[3:5] == 0).all()
+        assert torch.allclose(y[5:7], torch.tensor([178.0, 2e4]), rtol=2 ** -7) and y[7] == float("inf")
+
+
+def test_strided_rows_and_given_outputs():
+    M, K = 21, 384
+    wide = gen((M, 3 * K + 8), 12, "bf16")
+    for at in (0, 8, K, K + 3):                    # an offset of 3 leaves the vector path
+        x = wide[:, at:at + K]
+        q, s = dq.quantize_act_fp8_block(x)
+        q2, s2 = dq.quantize_act_fp8_block(x.contiguous())
+        assert torch.equal(q, q2) and torch.equal(s, s2)
+        assert torch.equal(dq.rmsnorm(x), dq.rmsnorm(x.contiguous()))
+        x2 = wide[:, at:at + 2 * K]
+        assert torch.equal(dq.silu_mul(x2), dq.silu_mul(x2.contiguous()))
+    x, r = gen((M, K), 13, "bf16"), gen((M, K), 14, "bf16")
+    ref = dq.rmsnorm(x, residual=r, quant="fp8_block")
+    out, sc = torch.empty((M, K), dtype=torch.uint8, device="cuda"), torch.empty((M, 3), device="cuda")
+    got = dq.rmsnorm(x, residual=r, quant="fp8_block", out=out, scales=sc, residual_out=r)   # in place
+    assert got[0] is out and got[1] is sc and got[2] is r
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("K", [256, 200])
+def test_special_values(K):
+    x = gen((6, K), 15, "fp32")
+    x[0] = 0
+    x[1, 130] = float("nan")
+    x[2, 3] = float("inf")
+    x[3, :128] = 1e-45                              # amax / 448 underflows: scale and codes 0
+    x[4, :128] = 1e-40                              # a subnormal scale
+    x[5, :128] = 3e38
+    q, s = dq.quantize_act_fp8_block(x)
+    v = F.e4m3_decode(q.cpu().numpy())
+    s = s.cpu().numpy()
+    assert (v[0] == 0).all() and (s[0] == 0).all()
+    assert np.isnan(s[1, 1]) and np.isnan(v[1, 128:]).all() and np.isfinite(v[1, :128]).all()
+    assert np.isinf(s[2, 0]) and np.isnan(v[2, 3]) and (np.delete(v[2, :128], 3) == 0).all()
+    assert s[3, 0] == 0 and (v[3, :128] == 0).all()
+    xs = x.double().cpu().numpy()
+    for row in (4, 5):
+        rq, rs = B.quantize_rows(xs[row:row + 1])
+        assert np.array_equal(s[row], rs[0]) and np.array_equal(q.cpu().numpy()[row], rq[0])
+    # a NaN or an infinity spoils its own row of the norm only
+    y = dq.rmsnorm(x, eps=1e-6).cpu()
+    assert (y[0] == 0).all() and torch.isnan(y[1]).all() and torch.isnan(y[2, 3]) and torch.isfinite(y[3:5]).all()
+
+
+def test_empty_batch():
+    x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    q, s = dq.quantize_act_fp8_block(x)
+    assert q.shape == (0, 256) and s.shape == (0, 2)
+    assert dq.rmsnorm(x, residual=x)[0].shape == (0, 256) and dq.silu_mul(x).shape == (0, 128)
+
+
+def test_offsets_past_32_bits():
+    M, K = 70000, 32768                             # 2.3e9 elements
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = gen((3, K), 16, "bf16")
+    q, s = dq.quantize_act_fp8_block(x)
+    q2, s2 = dq.quantize_act_fp8_block(x[-3:].contiguous())
+    assert torch.equal(q[-3:], q2) and torch.equal(s[-3:], s2) and not q[:-3].any()
+    n = dq.rmsnorm(x, out=x.clone())
+    assert torch.equal(n[-3:], dq.rmsnorm(x[-3:].contiguous()))
+
+
+def test_streams_and_graphs():
+    x, r = gen((64, 4096), 17, "bf16"), gen((64, 4096), 18, "bf16")
+    ref = dq.rmsnorm(x, residual=r, quant="fp8_block")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for kw, ctx in (({"stream": st}, torch.cuda.stream(torch.cuda.current_stream())), ({}, torch.cuda.stream(st))):
+        with ctx:
+            got = dq.rmsnorm(x, residual=r, quant="fp8_block", **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    outs = [torch.zeros_like(t) for t in ref]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dq.rmsnorm(x, residual=r, quant="fp8_block", out=outs[0], scales=outs[1], residual_out=outs[2])
+        dq.silu_mul(outs[2], quant="fp8_block")
+    x2 = gen((64, 4096), 19, "bf16")
+    want = dq.rmsnorm(x2, residual=r, quant="fp8_block")
+    x.copy_(x2)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs))

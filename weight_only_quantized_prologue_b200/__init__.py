@@ -24,6 +24,8 @@ from ._native import (  # noqa: F401
     dqgemm_pack_host,
     dqgemm_quantize_act_fp4,
     dqgemm_quantize_act_fp8,
+    dqgemm_quantize_act_fp8_block,
+    dqgemm_rmsnorm,
     dqgemm_run,
     dqgemm_run_fp8_static_quantized,
     dqgemm_run_fp8_static_quantized_out,
@@ -31,6 +33,7 @@ from ._native import (  # noqa: F401
     dqgemm_run_static_mlp,
     dqgemm_selftest_timeout,
     dqgemm_set_wait_limit,
+    dqgemm_silu_mul,
     dqgemm_status_string,
     storage_shapes,
 )
@@ -270,3 +273,18 @@ class QuantizedLinear:
             self.close()
         except Exception:
             pass
+
+
+_ROWS = ("rmsnorm", "silu_mul", "quantize_act_fp8_block")
+
+
+def __getattr__(name):
+    # the row operators need torch at import: loaded on first use, as the
+    # package itself does without it
+    if name in _ROWS:
+        from . import rows
+
+        for n in _ROWS:
+            globals()[n] = getattr(rows, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -39,7 +39,7 @@ class Plan(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
-_VP, _I, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+_VP, _I, _F, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
 _SIGNATURES = {
     "dqgemm_create": [ctypes.POINTER(_VP), _I, _I, _I, _VP, _VP, _F, _VP],
     "dqgemm_run": [_VP, _VP, _I, _VP, _VP],
@@ -58,6 +58,9 @@ _SIGNATURES = {
     "dqgemm_get_plan": [_VP, _I, ctypes.POINTER(Plan)],
     "dqgemm_set_wait_limit": [_VP, ctypes.c_longlong],
     "dqgemm_run_static_mlp": [_VP, _VP, _VP, _I, _VP, _VP, _VP],
+    "dqgemm_rmsnorm": [_I, _VP, _LL, _VP, _VP, _I, _VP, _F, _I, _I, _I, _F, _VP, _VP, _VP],
+    "dqgemm_silu_mul": [_I, _VP, _LL, _I, _I, _I, _F, _VP, _VP, _VP],
+    "dqgemm_quantize_act_fp8_block": [_I, _VP, _LL, _I, _I, _VP, _VP, _VP],
 }
 
 _lib = None
@@ -101,6 +104,23 @@ def _stream(stream):
         import torch
         return torch.cuda.current_stream().cuda_stream
     return int(stream) if not hasattr(stream, "cuda_stream") else stream.cuda_stream
+
+
+_raw_stream = None
+
+
+def device_stream(stream, dev):
+    """The stream argument of a call on device index `dev`: the given one, or
+    that device's current stream (looked up without building a Stream
+    object, which costs more than the rest of a small call)."""
+    global _raw_stream
+    if stream is not None:
+        return int(stream) if not hasattr(stream, "cuda_stream") else stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(dev)
 
 
 def storage_shapes(fmt, K, N):
@@ -176,6 +196,29 @@ def dqgemm_quantize_act_fp4(fmt, x, M, K, codes, scales, g_x=None, stream=None):
     float32 tensor of one element (NVFP4 formats)."""
     _check(lib().dqgemm_quantize_act_fp4(FORMATS[fmt], _ptr(x), int(M), int(K), _ptr(codes), _ptr(scales),
                                          _ptr(g_x), _stream(stream)), "dqgemm_quantize_act_fp4")
+
+
+# element types and output kinds of the row operators
+ROW_TYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
+ROW_OUTS = {"bf16": 0, "fp16": 1, "fp32": 2, "fp8_block": 3, "fp8_static": 4}
+
+
+def dqgemm_rmsnorm(type_, x, ldx, residual, residual_out, weight_type, weight, eps, M, K, out_kind, s_out, out,
+                   scales=None, stream=None):
+    """Types and out_kind by name (ROW_TYPES, ROW_OUTS)."""
+    _check(lib().dqgemm_rmsnorm(ROW_TYPES[type_], _ptr(x), ldx, _ptr(residual), _ptr(residual_out),
+                                ROW_TYPES[weight_type], _ptr(weight), eps, M, K, ROW_OUTS[out_kind], s_out, _ptr(out),
+                                _ptr(scales), _stream(stream)), "dqgemm_rmsnorm")
+
+
+def dqgemm_silu_mul(type_, x, ldx, M, K, out_kind, s_out, out, scales=None, stream=None):
+    _check(lib().dqgemm_silu_mul(ROW_TYPES[type_], _ptr(x), ldx, M, K, ROW_OUTS[out_kind], s_out, _ptr(out),
+                                 _ptr(scales), _stream(stream)), "dqgemm_silu_mul")
+
+
+def dqgemm_quantize_act_fp8_block(type_, x, ldx, M, K, q, scales, stream=None):
+    _check(lib().dqgemm_quantize_act_fp8_block(ROW_TYPES[type_], _ptr(x), ldx, M, K, _ptr(q), _ptr(scales),
+                                               _stream(stream)), "dqgemm_quantize_act_fp8_block")
 
 
 def dqgemm_pack_host(fmt, W):

@@ -12,66 +12,12 @@
 #include "dq_aux.cuh"
 #include "dq_codec.h"
 #include "dq_gemm.cuh"
+#include "dq_handle.h"
 #include "dqgemm.h"
 
 using namespace dq;
 
-struct dqgemm_s {
-  int fmt = 0, K = 0, N = 0;
-  int k_stages = 0, n_tiles = 0;
-  int device = 0, num_sms = 0;
-  uint8_t* wchunks = nullptr;       // pre-tiled weight
-  size_t wchunk_bytes = 0;
-  float* col_scale = nullptr;       // [N] for FP8 formats
-  __nv_bfloat16* bias = nullptr;    // [N] or null
-  int* status = nullptr;            // status word as the device addresses it
-  int* status_host = nullptr;       //   ... and as the host reads it (mapped pinned memory)
-  float sigma = 1.f, s_x = 1.f;
-  int mx_bias = 126;
-  long long weight_bytes = 0;       // canonical packed + scale bytes
-  int max_clusters[4][9] = {};      // co-resident clusters per (BN index, cluster size), 0 = unknown
-  // FP4 x FP4: the activation workspace (codes, scale words, the NVFP4 amax
-  // partials, ticket and g_x), grown on demand and reused by every call
-  uint8_t* ws = nullptr;
-  size_t ws_bytes = 0;
-  unsigned long long timeout_ns = 0;  // limit of the kernels' pipeline waits
-  // activation tensor maps already encoded, by (x, M, tile rows, e4m3 input):
-  // encoding one costs host time on every call, and layers see the same
-  // few activation buffers again and again
-  struct MapEntry {
-    const void* x = nullptr;
-    int M = 0, bn = 0;
-    bool xq = false, x3d = false;
-    CUtensorMap map;
-  };
-  static constexpr int kMaps = 8;
-  MapEntry maps[kMaps];
-  int next_map = 0;
-  std::mutex maps_mu;               // run entry points may be called from several threads
-};
-
 namespace {
-
-constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;   // 2 s
-
-unsigned long long timeout_ns() {
-  static unsigned long long t = [] {
-    const char* e = std::getenv("DQGEMM_TIMEOUT_MS");
-    return e ? (unsigned long long)std::strtoull(e, nullptr, 10) * 1000000ull : kDefaultTimeoutNs;
-  }();
-  return t;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool is_device_ptr(const void* p) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
-}
 
 // canonical storage sizes of dqgemm.h
 // the canonical storage of a W4A4 handle is that of its weight format
@@ -206,21 +152,6 @@ void relayout(int fmt, int K, int N, int KS, int NT, const std::vector<uint8_t>&
 // ---------------------------------------------------------------------------
 // tensor map for the bf16 activation x [M, K]: boxes of 64 k x BN rows, 128B swizzle
 // ---------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
 
 // With K a multiple of 64 the map is 3-D {64, M, K/64} (the k-blocks are
 // 128 bytes apart) so one box {64, bn, 2} brings a whole 128-k stage.
@@ -246,30 +177,9 @@ bool make_x_map(CUtensorMap* map, const void* x, int M, int K, int bn, bool* is3
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// e4m3 activations [M, K] (u8, K % 16 == 0): box of 128 k x bn rows, the
-// tensor core's 128-byte-swizzled K-major image
-bool make_q_map(CUtensorMap* map, const void* q, int M, int K, int bn) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M};
-  const cuuint64_t strides[1] = {(cuuint64_t)K};
-  const cuuint32_t box[2] = {128, (cuuint32_t)bn};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // ---------------------------------------------------------------------------
 // launch dispatch
 // ---------------------------------------------------------------------------
-bool pdl_enabled() {
-  static bool on = [] {
-    const char* e = std::getenv("DQGEMM_PDL");
-    return !(e && e[0] == '0');
-  }();
-  return on;
-}
 
 template <int FMT, int BN>
 struct GemmLauncher {
@@ -571,34 +481,12 @@ bool x_map(dqgemm_s* h, const void* x, int M, int bn, bool xq, CUtensorMap* tm, 
   return true;
 }
 
-dqgemm_status cuda_err(cudaError_t e) { return e == cudaSuccess ? DQ_OK : DQ_ERR_CUDA; }
-
 // f32(1 / s), correctly rounded (an IEEE fp32 division on the host): the
 // reciprocal the kernels' static-FP8 quantizers multiply by
 float recip_rn(float s) {
   volatile float one = 1.f;
   volatile float r = one / s;
   return r;
-}
-
-// a small kernel in the programmatic-dependent-launch chain of the GEMMs
-// (its first instruction waits for the previous grid)
-template <typename... KArgs, typename... Args>
-cudaError_t launch_chained(void (*kern)(KArgs...), int grid, int block, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.stream = st;
-  cudaLaunchAttribute a[1];
-  int na = 0;
-  if (pdl_enabled()) {
-    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a[0].val.programmaticStreamSerializationAllowed = 1;
-    na = 1;
-  }
-  cfg.attrs = a;
-  cfg.numAttrs = na;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
 int act_amax_grid(long long count) {

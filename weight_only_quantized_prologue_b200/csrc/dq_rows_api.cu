@@ -1,0 +1,165 @@
+// dq_rows_api.cu -- the row operators of include/dqgemm.h: dqgemm_rmsnorm,
+// dqgemm_silu_mul, dqgemm_quantize_act_fp8_block.
+#include <algorithm>
+#include <cmath>
+
+#include "dq_handle.h"
+#include "dq_rows.cuh"
+
+using namespace dq;
+
+namespace {
+
+size_t type_bytes(int t) { return t == ROW_FP32 ? 4 : 2; }
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+size_t out_bytes(int out) { return out == OUT_FP32 ? 4 : out <= OUT_FP16 ? 2 : 1; }
+
+// Natural alignment of every buffer; *al: whether whole 16-byte vectors can
+// be moved (8-byte ones for codes).
+dqgemm_status check_rows(const RowArgs& a, int type, int out, int halves, bool* al) {
+  if (type < ROW_BF16 || type > ROW_FP32 || out < OUT_BF16 || out > OUT_STATIC) return DQ_ERR_INVALID_ARG;
+  if (!a.x || !a.out || a.M < 1 || a.K < 1 || a.K > (1 << 28) || a.ldx < (long long)halves * a.K)
+    return DQ_ERR_INVALID_ARG;
+  if (out == OUT_BLOCK && !a.scales) return DQ_ERR_INVALID_ARG;
+  if (out == OUT_STATIC && !(std::isfinite(a.s_out) && a.s_out > 0.f)) return DQ_ERR_INVALID_ARG;
+  const size_t tb = type_bytes(type), ob = out_bytes(out);
+  if (!aligned_to(a.x, tb) || !aligned_to(a.out, ob) || (out == OUT_BLOCK && !aligned_to(a.scales, 4)) ||
+      (a.res && (!aligned_to(a.res, tb) || !aligned_to(a.res_out, tb))) || (a.w && !aligned_to(a.w, type_bytes(a.w_type))))
+    return DQ_ERR_ALIGNMENT;
+  *al = a.K % 8 == 0 && aligned16(a.x) && (a.ldx * (long long)tb) % 16 == 0 && aligned_to(a.out, ob == 1 ? 8 : 16) &&
+        (!a.res || (aligned16(a.res) && aligned16(a.res_out))) && (!a.w || aligned16(a.w));
+  return DQ_OK;
+}
+
+template <typename... KArgs, typename... Args>
+dqgemm_status launch_rows(void (*kern)(KArgs...), dim3 grid, dim3 block, void* stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cuda_err(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...));
+}
+
+template <typename T, int OUT, bool AL>
+dqgemm_status norm_launch(const RowArgs& a, void* stream) {
+  // threads a row: one vector each up to 512 of them (K = 4096), then 2 and 4
+  // vectors each; longer rows are read twice
+  const int vecs = (a.K + 7) / 8;
+  int tpr = 32;
+  while (tpr < 512 && tpr < vecs) tpr *= 2;
+  const int per = (vecs + tpr - 1) / tpr;
+  const int rows = std::max(1, 128 / tpr);
+  const dim3 block(tpr, rows);
+  const dim3 grid((unsigned)((a.M + rows - 1) / rows));
+  if (per <= 1) return launch_rows(rmsnorm_kernel<T, 1, OUT, AL>, grid, block, stream, a);
+  if (per <= 2) return launch_rows(rmsnorm_kernel<T, 2, OUT, AL>, grid, block, stream, a);
+  if (per <= 4) return launch_rows(rmsnorm_kernel<T, 4, OUT, AL>, grid, block, stream, a);
+  return launch_rows(rmsnorm_kernel<T, 0, OUT, AL>, grid, block, stream, a);
+}
+
+template <typename T, bool GATE, int OUT, bool AL>
+dqgemm_status plain_launch(const RowArgs& a, void* stream) {
+  const int chunks = ((a.K + 7) / 8 + 255) / 256;
+  const long long ctas = (long long)chunks * a.M;
+  if (ctas > 0x7FFFFFFFll) return DQ_ERR_UNSUPPORTED;
+  return launch_rows(rows_kernel<T, GATE, OUT, AL>, dim3((unsigned)ctas), dim3(256), stream, a, chunks);
+}
+
+// OP 0: rmsnorm, 1: gated SiLU, 2: plain (block-quantized output only)
+template <int OP, typename T, int OUT>
+dqgemm_status go(const RowArgs& a, bool al, void* stream) {
+  if constexpr (OP == 0)
+    return al ? norm_launch<T, OUT, true>(a, stream) : norm_launch<T, OUT, false>(a, stream);
+  else
+    return al ? plain_launch<T, OP == 1, OUT, true>(a, stream) : plain_launch<T, OP == 1, OUT, false>(a, stream);
+}
+
+template <int OP, typename T>
+dqgemm_status go_out(const RowArgs& a, int out, bool al, void* stream) {
+  if constexpr (OP == 2) {
+    return go<OP, T, OUT_BLOCK>(a, al, stream);
+  } else {
+    switch (out) {
+      case OUT_BF16: return go<OP, T, OUT_BF16>(a, al, stream);
+      case OUT_FP16: return go<OP, T, OUT_FP16>(a, al, stream);
+      case OUT_FP32: return go<OP, T, OUT_FP32>(a, al, stream);
+      case OUT_BLOCK: return go<OP, T, OUT_BLOCK>(a, al, stream);
+      default: return go<OP, T, OUT_STATIC>(a, al, stream);
+    }
+  }
+}
+
+template <int OP>
+dqgemm_status run_rows(RowArgs& a, int type, int out, float s_out, void* stream) {
+  a.s_out = out == OUT_STATIC ? s_out : 1.f;
+  bool al = false;
+  const dqgemm_status st = check_rows(a, type, out, OP == 1 ? 2 : 1, &al);
+  if (st != DQ_OK) return st;
+  volatile float one = 1.f;
+  volatile float r = one / a.s_out;   // an fp32 division
+  a.r_out = r;
+  switch (type) {
+    case ROW_BF16: return go_out<OP, __nv_bfloat16>(a, out, al, stream);
+    case ROW_FP16: return go_out<OP, __half>(a, out, al, stream);
+    default: return go_out<OP, float>(a, out, al, stream);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+dqgemm_status dqgemm_rmsnorm(dqgemm_dtype type, const void* x, long long ldx, const void* residual,
+                             void* residual_out, dqgemm_dtype weight_type, const void* weight, float eps, int M, int K,
+                             dqgemm_out out_kind, float s_out, void* out, float* scales, void* stream) {
+  if ((residual == nullptr) != (residual_out == nullptr)) return DQ_ERR_INVALID_ARG;
+  if (residual_out && residual_out == out) return DQ_ERR_INVALID_ARG;
+  if ((int)weight_type < ROW_BF16 || (int)weight_type > ROW_FP32) return DQ_ERR_INVALID_ARG;
+  if (!(std::isfinite(eps) && eps >= 0.f)) return DQ_ERR_INVALID_ARG;
+  RowArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.res = residual;
+  a.res_out = residual_out;
+  a.w = weight;
+  a.w_type = (int)weight_type;
+  a.eps = eps;
+  a.M = M;
+  a.K = K;
+  a.out = out;
+  a.scales = scales;
+  return run_rows<0>(a, (int)type, (int)out_kind, s_out, stream);
+}
+
+dqgemm_status dqgemm_silu_mul(dqgemm_dtype type, const void* x, long long ldx, int M, int K, dqgemm_out out_kind,
+                              float s_out, void* out, float* scales, void* stream) {
+  RowArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.M = M;
+  a.K = K;
+  a.out = out;
+  a.scales = scales;
+  return run_rows<1>(a, (int)type, (int)out_kind, s_out, stream);
+}
+
+dqgemm_status dqgemm_quantize_act_fp8_block(dqgemm_dtype type, const void* x, long long ldx, int M, int K, void* q,
+                                            float* scales, void* stream) {
+  RowArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.M = M;
+  a.K = K;
+  a.out = q;
+  a.scales = scales;
+  return run_rows<2>(a, (int)type, OUT_BLOCK, 1.f, stream);
+}
+
+}  // extern "C"
