@@ -95,6 +95,14 @@ extern "C" {
  *                  (global_scale = g_w); x quantized per call with its own
  *                  global scale g_x = amax(x) / 2688 and E4M3 scales per 16.
  *                  K % 16 == 0, N % 16 == 0
+ *   DQ_FP8_BLOCK128  e4m3 with a scale per block on both sides: packed u8
+ *                  [N, K] e4m3 codes; scales fp32 [ceil(N/128), ceil(K/128)],
+ *                  one per 128 x 128 block (finite, >= 0); activations e4m3
+ *                  with an fp32 scale per 128 along K, either quantized per
+ *                  call (dqgemm_run) or given as codes
+ *                  (dqgemm_run_fp8_block_quantized).  The products of a block
+ *                  are summed in fp32 by the tensor core, scaled and summed
+ *                  over the blocks in fp32.  K % 16 == 0, any N
  */
 typedef enum {
   DQ_INT4_G128 = 0,
@@ -104,7 +112,8 @@ typedef enum {
   DQ_FP8_STATIC = 4,
   DQ_INT4_ASYM_G128 = 5,
   DQ_W4A4_MXFP4 = 6,
-  DQ_W4A4_NVFP4 = 7
+  DQ_W4A4_NVFP4 = 7,
+  DQ_FP8_BLOCK128 = 8
 } dqgemm_format;
 
 typedef enum {
@@ -206,6 +215,35 @@ dqgemm_status dqgemm_run_fp8_static_quantized_out(dqgemm_handle h, const void* q
 dqgemm_status dqgemm_run_static_mlp(dqgemm_handle l1, dqgemm_handle l2, const void* x, int M,
                                     void* h_out, void* y, void* stream);
 
+/* DQ_FP8_BLOCK128 only: the product on activations that are already codes,
+ * q u8 [M, K] with scales fp32 [M, ceil(K/128)] as dqgemm_quantize_act_fp8_block,
+ * dqgemm_rmsnorm and dqgemm_silu_mul write them.  y: device bf16 [M, N].  One
+ * launch, no workspace: calls on one handle may run on several streams at
+ * once.  (dqgemm_run on such a handle quantizes x into a workspace of the
+ * handle first and is bound by what it says about W4A4 handles: first call of
+ * the largest M before any capture, calls stream-ordered.)
+ * DQ_ERR_UNSUPPORTED for other formats and for experts. */
+dqgemm_status dqgemm_run_fp8_block_quantized(dqgemm_handle h, const void* q, const float* scales, int M, void* y,
+                                             void* stream);
+
+/* A handle of E weights of one shape ("experts"), for products whose rows are
+ * grouped by expert.  packed_w, scales and bias are the E weights' canonical
+ * buffers one after the other: u8 [E, N, K], fp32 [E, ceil(N/128),
+ * ceil(K/128)], bf16 [E, N] or NULL; copied as by dqgemm_create.  fmt:
+ * DQ_FP8_BLOCK128 (others: DQ_ERR_UNSUPPORTED); 1 <= E <= 1024. */
+dqgemm_status dqgemm_create_experts(dqgemm_handle* out, dqgemm_format fmt, int E, int K, int N, const void* packed_w,
+                                    const void* scales, const void* bias);
+
+/* y[m] = x[m] . deq(W_e)^T + b_e for the rows offsets[e] <= m < offsets[e+1] of
+ * every expert e; x as codes and scales (see dqgemm_run_fp8_block_quantized).
+ * offsets: device int32 [E + 1], not decreasing; read on the device, so the
+ * host need not know them, and they may change between replays of a graph.
+ * Experts without rows cost nothing; rows of y that no expert has are left as
+ * they were.  Offsets outside [0, M] count as the nearest end, and an expert
+ * whose end lies before its start has no rows.  One launch, no workspace. */
+dqgemm_status dqgemm_run_experts_quantized(dqgemm_handle h, const void* q, const float* scales, int M, const int* offsets,
+                                           void* y, void* stream);
+
 /* Release the handle and its device memory.  Synchronizes the device (the
  * CUDA runtime's cudaFree does so in any case); no kernel of the handle may
  * still be queued or running. */
@@ -214,7 +252,8 @@ dqgemm_status dqgemm_destroy(dqgemm_handle h);
 /* Debug: write the dequantized weight as bf16 [N, K] (device) from the
  * handle's re-laid-out storage, through the same unpack code the GEMM
  * prologue uses:  INT4 bf16(c*s);  NVFP4 bf16(f32(e2m1*dec(sb)*g));
- * MXFP4 bf16(e2m1*2^(e-127));  FP8 bf16(f32(e4m3*s[n])).  -0.0 is kept. */
+ * MXFP4 bf16(e2m1*2^(e-127));  FP8 bf16(f32(e4m3*s[n])), block-scaled FP8
+ * bf16(f32(e4m3*s[n/128,k/128])) (experts: [E, N, K]).  -0.0 is kept. */
 dqgemm_status dqgemm_dequantize(dqgemm_handle h, void* w_bf16, void* stream);
 
 /* Static-FP8 activation quantization (the Q node of the static FP8 page's
@@ -299,6 +338,8 @@ dqgemm_status dqgemm_quantize_act_fp8_block(dqgemm_dtype type, const void* x, lo
  *   MXFP4  e = floor(log2 amax_blk32) - 2 in [-127,127]; code e+127 (0 for a
  *          zero block); c = e2m1(W * 2^-e), saturating
  *   FP8    s[n] = max|W[n,:]|/448; c = e4m3(W/s[n]) (0 for a zero row)
+ *   FP8 block  s = amax of the 128 x 128 block / 448; c = e4m3(W/s) (0 for a
+ *          zero block)
  *   INT4 asymmetric  lo = min(0, min W), hi = max(0, max W) per group;
  *          s = bf16(f32(hi - lo)/15); z = clamp(rne(-lo/s), 0, 15);
  *          c = clamp(rne(W/s) + z, 0, 15); s == 0 -> c = 0, z = 0; a group

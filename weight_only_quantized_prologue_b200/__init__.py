@@ -15,6 +15,7 @@ from ._native import (  # noqa: F401
     FORMATS,
     DQError,
     dqgemm_create,
+    dqgemm_create_experts,
     dqgemm_dequantize,
     dqgemm_destroy,
     dqgemm_get_plan,
@@ -27,6 +28,8 @@ from ._native import (  # noqa: F401
     dqgemm_quantize_act_fp8_block,
     dqgemm_rmsnorm,
     dqgemm_run,
+    dqgemm_run_experts_quantized,
+    dqgemm_run_fp8_block_quantized,
     dqgemm_run_fp8_static_quantized,
     dqgemm_run_fp8_static_quantized_out,
     dqgemm_run_quantized_out,
@@ -109,6 +112,32 @@ def static_mlp(l1, l2, x, out=None, h_out=None, stream=None):
         return out
     dqgemm_run_static_mlp(l1.handle, l2.handle, x, M, h_out, out, stream)
     return out
+
+
+def _block_call(layer, x, M, offsets, out, stream):
+    """A block-scaled layer (or experts, with their offsets) on bf16 x:
+    quantize, then the product.  The codes and scales between the two live in
+    one temporary of the stream the calls run on, so that the allocator hands
+    it to nobody before they are done."""
+    torch = _torch()
+    L, dev, K = _native.lib(), layer._dev, layer.K
+    s = _native.device_stream(stream, dev)
+    nq = (M * K + 255) // 256 * 256
+    size = nq + 4 * M * ((K + 127) // 128)
+    if stream is None:
+        tmp = torch.empty(size, dtype=torch.uint8, device=layer.device)
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(s, device=layer.device)):
+            tmp = torch.empty(size, dtype=torch.uint8, device=layer.device)
+    q = tmp.data_ptr()
+    _native._check(L.dqgemm_quantize_act_fp8_block(0, x.data_ptr(), K, M, K, q, q + nq, s),
+                   "dqgemm_quantize_act_fp8_block")
+    if offsets is None:
+        _native._check(L.dqgemm_run_fp8_block_quantized(layer._h, q, q + nq, M, out.data_ptr(), s),
+                       "dqgemm_run_fp8_block_quantized")
+    else:
+        _native._check(L.dqgemm_run_experts_quantized(layer._h, q, q + nq, M, offsets.data_ptr(), out.data_ptr(), s),
+                       "dqgemm_run_experts_quantized")
 
 
 class QuantizedLinear:
@@ -196,7 +225,9 @@ class QuantizedLinear:
         out = self._out(out, M, torch.bfloat16)
         if M == 0:
             return out
-        if self.fmt == "fp8_static" and M >= self._static_prequant_m:
+        if self.fmt == "fp8_block":
+            _block_call(self, x, M, None, out, stream)
+        elif self.fmt == "fp8_static" and M >= self._static_prequant_m:
             q = torch.empty((M, self.K), dtype=torch.uint8, device=self.device)
             dqgemm_quantize_act_fp8(x, M, self.K, self.act_scale, q, stream)
             dqgemm_run_fp8_static_quantized(self._h, q, M, out, stream)
@@ -221,16 +252,26 @@ class QuantizedLinear:
             dqgemm_run_quantized_out(self._h, x, M, out, s_out, stream)
         return out
 
-    def from_codes(self, q, out=None, stream=None):
-        """Static FP8 only: the layer on activations already quantized with
-        its own scale (uint8 e4m3 codes [M, K], e.g. from quantized_out)."""
-        import torch
-
-        if self.fmt != "fp8_static":
-            raise ValueError("from_codes needs a static FP8 layer")
+    def from_codes(self, q, out=None, stream=None, scales=None):
+        """The layer on activations that are e4m3 codes already (uint8 [M, K]):
+        static FP8, quantized with the layer's own scale (e.g. by
+        quantized_out); "fp8_block", with their ``scales`` fp32 [M, ceil(K /
+        128)] (from rmsnorm, silu_mul or quantize_act_fp8_block)."""
+        torch = _torch()
+        if self.fmt not in ("fp8_static", "fp8_block"):
+            raise ValueError("from_codes needs a static FP8 layer or a block-scaled one")
+        if (scales is None) == (self.fmt == "fp8_block"):
+            raise ValueError("scales go with the codes of an fp8_block layer")
         M = self._check_x(q, torch.uint8, "q")
+        if scales is not None and not _fits(scales, (self.K + 127) // 128, torch.float32, M, self._dev):
+            _require(scales, "scales", shape=(M, (self.K + 127) // 128), dtype=torch.float32, device=self.device)
         out = self._out(out, M, torch.bfloat16)
         if M == 0:
+            return out
+        if scales is not None:
+            _native._check(_native.lib().dqgemm_run_fp8_block_quantized(
+                self._h, q.data_ptr(), scales.data_ptr(), M, out.data_ptr(), _native.device_stream(stream, self._dev)),
+                "dqgemm_run_fp8_block_quantized")
             return out
         dqgemm_run_fp8_static_quantized(self._h, q, M, out, stream)
         return out
@@ -273,6 +314,104 @@ class QuantizedLinear:
             self.close()
         except Exception:
             pass
+
+
+class QuantizedExperts:
+    """E quantized Linear weights of one shape on the current CUDA device, for
+    rows that are grouped by expert: rows ``offsets[e] .. offsets[e + 1]`` go
+    through weight e.
+
+    fmt: "fp8_block".  ``packed`` uint8 [E, N, K] and ``scales`` fp32 [E,
+    ceil(N / 128), ceil(K / 128)] are the weights' canonical storage (see
+    ``storage_shapes``), ``bias`` bf16 [E, N] or None; all copied."""
+
+    def __init__(self, fmt, E, K, N, packed, scales, bias=None):
+        import torch
+
+        self._h = None
+        if fmt != "fp8_block":
+            raise ValueError(f"experts take the format 'fp8_block', not {fmt!r}")
+        _require(packed, "packed", shape=(E, N, K), dtype=torch.uint8)
+        _require(scales, "scales", shape=(E, (N + 127) // 128, (K + 127) // 128), dtype=torch.float32,
+                 device=packed.device)
+        if bias is not None:
+            _require(bias, "bias", shape=(E, N), dtype=torch.bfloat16, device=packed.device)
+        self.fmt, self.E, self.K, self.N = fmt, E, K, N
+        self.device = packed.device
+        self._dev = self.device.index
+        self._check_current = torch.cuda.device_count() > 1
+        self._h = dqgemm_create_experts(fmt, E, K, N, packed, scales, bias)
+
+    @classmethod
+    def from_float(cls, fmt, W, bias=None):
+        """Quantize CUDA weights [E, N, K] with the GPU packer."""
+        import torch
+
+        if not getattr(W, "is_cuda", False) or W.dim() != 3:
+            raise ValueError("W must be a 3-D CUDA tensor [E, N, K]")
+        if fmt != "fp8_block":
+            raise ValueError(f"experts take the format 'fp8_block', not {fmt!r}")
+        E, N, K = W.shape
+        ps, _, ss, _ = storage_shapes(fmt, K, N)
+        packed = torch.empty((E, *ps), dtype=torch.uint8, device=W.device)
+        scales = torch.empty((E, *ss), dtype=torch.float32, device=W.device)
+        for e in range(E):
+            dqgemm_pack_device_noalloc(fmt, W[e].detach().to(torch.float32).contiguous(), packed[e], scales[e])
+        return cls(fmt, E, K, N, packed, scales, bias)
+
+    # checks and results of one [M, K] operand, as a layer's
+    _check_x = QuantizedLinear._check_x
+    _out = QuantizedLinear._out
+
+    def _check_offsets(self, offsets):
+        torch = _torch()
+        _require(offsets, "offsets", shape=(self.E + 1,), dtype=torch.int32, device=self.device)
+
+    def __call__(self, x, offsets, out=None, stream=None):
+        """y[m] = x[m] . deq(W_e)^T + b_e for offsets[e] <= m < offsets[e + 1];
+        x bf16 [M, K], offsets int32 [E + 1] on the device, not decreasing; y
+        (``out``, allocated if None) bf16 [M, N].  Rows that no expert has are
+        left as they were (undefined in an allocated y)."""
+        torch = _torch()
+        M = self._check_x(x, torch.bfloat16)
+        self._check_offsets(offsets)
+        out = self._out(out, M, torch.bfloat16)
+        if M:
+            _block_call(self, x, M, offsets, out, stream)
+        return out
+
+    def from_codes(self, q, scales, offsets, out=None, stream=None):
+        """The same on e4m3 codes uint8 [M, K] with scales fp32 [M, ceil(K / 128)]."""
+        torch = _torch()
+        M = self._check_x(q, torch.uint8, "q")
+        _require(scales, "scales", shape=(M, (self.K + 127) // 128), dtype=torch.float32, device=self.device)
+        self._check_offsets(offsets)
+        out = self._out(out, M, torch.bfloat16)
+        if M:
+            _native._check(_native.lib().dqgemm_run_experts_quantized(
+                self._h, q.data_ptr(), scales.data_ptr(), M, offsets.data_ptr(), out.data_ptr(),
+                _native.device_stream(stream, self._dev)), "dqgemm_run_experts_quantized")
+        return out
+
+    def dequantize(self, stream=None):
+        w = _torch().empty((self.E, self.N, self.K), dtype=_torch().bfloat16, device=self.device)
+        dqgemm_dequantize(self._h, w, stream)
+        return w
+
+    plan = QuantizedLinear.plan
+    last_error = QuantizedLinear.last_error
+    handle = QuantizedLinear.handle
+    close = QuantizedLinear.close
+    __del__ = QuantizedLinear.__del__
+
+    def __copy__(self):
+        raise TypeError("QuantizedExperts owns a device handle and cannot be copied; build another one")
+
+    def __deepcopy__(self, memo):
+        self.__copy__()
+
+    def __reduce__(self):
+        raise TypeError("QuantizedExperts owns a device handle and cannot be pickled")
 
 
 _ROWS = ("rmsnorm", "silu_mul", "quantize_act_fp8_block")

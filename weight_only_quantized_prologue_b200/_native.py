@@ -15,7 +15,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdqgemm.so")
 
 FORMATS = {"int4": 0, "nvfp4": 1, "mxfp4": 2, "fp8": 3, "fp8_static": 4, "int4_asym": 5,
-           "w4a4_mxfp4": 6, "w4a4_nvfp4": 7}
+           "w4a4_mxfp4": 6, "w4a4_nvfp4": 7, "fp8_block": 8}
 STATUS_NAMES = {0: "DQ_OK", 1: "DQ_ERR_INVALID_ARG", 2: "DQ_ERR_UNSUPPORTED", 3: "DQ_ERR_ALIGNMENT",
                 4: "DQ_ERR_ALLOC", 5: "DQ_ERR_CUDA", 6: "DQ_ERR_TIMEOUT"}
 DQ_OK, DQ_ERR_INVALID_ARG, DQ_ERR_UNSUPPORTED, DQ_ERR_ALIGNMENT = 0, 1, 2, 3
@@ -58,6 +58,9 @@ _SIGNATURES = {
     "dqgemm_get_plan": [_VP, _I, ctypes.POINTER(Plan)],
     "dqgemm_set_wait_limit": [_VP, ctypes.c_longlong],
     "dqgemm_run_static_mlp": [_VP, _VP, _VP, _I, _VP, _VP, _VP],
+    "dqgemm_run_fp8_block_quantized": [_VP, _VP, _VP, _I, _VP, _VP],
+    "dqgemm_create_experts": [ctypes.POINTER(_VP), _I, _I, _I, _I, _VP, _VP, _VP],
+    "dqgemm_run_experts_quantized": [_VP, _VP, _VP, _I, _VP, _VP, _VP],
     "dqgemm_rmsnorm": [_I, _VP, _LL, _VP, _VP, _I, _VP, _F, _I, _I, _I, _F, _VP, _VP, _VP],
     "dqgemm_silu_mul": [_I, _VP, _LL, _I, _I, _I, _F, _VP, _VP, _VP],
     "dqgemm_quantize_act_fp8_block": [_I, _VP, _LL, _I, _I, _VP, _VP, _VP],
@@ -133,6 +136,8 @@ def storage_shapes(fmt, K, N):
         return (N, K // 2), np.uint8, (N, K // 16), np.uint8
     if fmt in ("mxfp4", "w4a4_mxfp4"):
         return (N, K // 2), np.uint8, (N, K // 32), np.uint8
+    if fmt == "fp8_block":   # one scale per 128 x 128 block
+        return (N, K), np.uint8, ((N + 127) // 128, (K + 127) // 128), np.float32
     return (N, K), np.uint8, (N,), np.float32
 
 
@@ -196,6 +201,23 @@ def dqgemm_quantize_act_fp4(fmt, x, M, K, codes, scales, g_x=None, stream=None):
     float32 tensor of one element (NVFP4 formats)."""
     _check(lib().dqgemm_quantize_act_fp4(FORMATS[fmt], _ptr(x), int(M), int(K), _ptr(codes), _ptr(scales),
                                          _ptr(g_x), _stream(stream)), "dqgemm_quantize_act_fp4")
+
+
+def dqgemm_run_fp8_block_quantized(h, q, scales, M, y, stream=None):
+    _check(lib().dqgemm_run_fp8_block_quantized(h, _ptr(q), _ptr(scales), int(M), _ptr(y), _stream(stream)),
+           "dqgemm_run_fp8_block_quantized")
+
+
+def dqgemm_create_experts(fmt, E, K, N, packed_w, scales, bias=None):
+    h = ctypes.c_void_p()
+    _check(lib().dqgemm_create_experts(ctypes.byref(h), FORMATS[fmt], E, K, N, _ptr(packed_w), _ptr(scales), _ptr(bias)),
+           "dqgemm_create_experts")
+    return h
+
+
+def dqgemm_run_experts_quantized(h, q, scales, M, offsets, y, stream=None):
+    _check(lib().dqgemm_run_experts_quantized(h, _ptr(q), _ptr(scales), int(M), _ptr(offsets), _ptr(y), _stream(stream)),
+           "dqgemm_run_experts_quantized")
 
 
 # element types and output kinds of the row operators

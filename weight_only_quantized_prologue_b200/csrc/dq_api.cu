@@ -21,6 +21,11 @@ namespace {
 
 // canonical storage sizes of dqgemm.h
 // the canonical storage of a W4A4 handle is that of its weight format
+// public format -> internal (-1: unknown)
+int internal_fmt(int fmt) {
+  return fmt == DQ_FP8_BLOCK128 ? FMT_FP8B : fmt >= 0 && fmt <= FMT_W4A4NV ? fmt : -1;
+}
+
 int storage_fmt(int fmt) { return fmt == FMT_W4A4MX ? FMT_MXFP4 : fmt == FMT_W4A4NV ? FMT_NVFP4 : fmt; }
 
 size_t packed_bytes(int fmt, int K, int N) {
@@ -39,7 +44,7 @@ size_t scale_bytes(int fmt, int K, int N) {
 }
 
 dqgemm_status check_shape(int fmt, int K, int N) {
-  if (fmt < 0 || fmt > FMT_W4A4NV || K <= 0 || N <= 0) return DQ_ERR_INVALID_ARG;
+  if (fmt < 0 || (fmt > FMT_W4A4NV && fmt != FMT_FP8B) || K <= 0 || N <= 0) return DQ_ERR_INVALID_ARG;
   switch (storage_fmt(fmt)) {
     case FMT_INT4:
     case FMT_INT4A: return K % 128 ? DQ_ERR_INVALID_ARG : DQ_OK;
@@ -570,9 +575,10 @@ dqgemm_status dqgemm_create(dqgemm_handle* out, dqgemm_format fmt_, int K, int N
                             const void* scales, float global_scale, const void* bias) {
   if (!out) return DQ_ERR_INVALID_ARG;
   *out = nullptr;
-  const int fmt = (int)fmt_;
+  const int fmt = internal_fmt((int)fmt_);
   dqgemm_status st = check_shape(fmt, K, N);
   if (st != DQ_OK) return st;
+  if (fmt == FMT_FP8B) return block_create(out, 1, K, N, packed_w, scales, bias);
   if (!packed_w || !scales) return DQ_ERR_INVALID_ARG;
   if (!aligned16(packed_w) || !aligned16(scales) || (bias && !aligned16(bias))) return DQ_ERR_ALIGNMENT;
   if (!is_device_ptr(packed_w) || !is_device_ptr(scales) || (bias && !is_device_ptr(bias)))
@@ -652,6 +658,10 @@ dqgemm_status dqgemm_set_wait_limit(dqgemm_handle h, long long timeout_ns_) {
 
 dqgemm_status dqgemm_get_plan(dqgemm_handle h, int M, dqgemm_plan* plan) {
   if (!h || !plan || M < 1) return DQ_ERR_INVALID_ARG;
+  if (h->fmt == FMT_FP8B) {
+    block_fill_plan(h, M, plan);
+    return DQ_OK;
+  }
   fill_plan(h, M, plan);
   return DQ_OK;
 }
@@ -732,6 +742,10 @@ static dqgemm_status run_w4a4(dqgemm_handle h, const void* x, int M, void* y, vo
 static dqgemm_status run_gemm(dqgemm_handle h, const void* x, bool xq, int M, void* y, bool yq, float s_out,
                               void* stream) {
   if (!h || !x || !y || M < 1) return DQ_ERR_INVALID_ARG;
+  if (h->fmt == FMT_FP8B) {
+    if (xq || yq || h->E != 1) return DQ_ERR_UNSUPPORTED;
+    return block_run_x(h, x, M, y, stream);
+  }
   if (is_w4a4(h->fmt)) {
     if (xq || yq) return DQ_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(y)) return DQ_ERR_ALIGNMENT;
@@ -860,6 +874,7 @@ void launch_dequant(const dqgemm_s* h, float sigma, __nv_bfloat16* o, cudaStream
 
 dqgemm_status dqgemm_dequantize(dqgemm_handle h, void* w_bf16, void* stream) {
   if (!h || !w_bf16) return DQ_ERR_INVALID_ARG;
+  if (h->fmt == FMT_FP8B) return block_dequantize(h, w_bf16, stream);
   if (is_w4a4(h->fmt)) return DQ_ERR_UNSUPPORTED;   // no bf16 operand: the tensor core reads the codes
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(w_bf16);
@@ -903,7 +918,7 @@ static __device__ __align__(256) float g_act_fp4_scratch[kActAmaxBlocks + 4];
 
 dqgemm_status dqgemm_quantize_act_fp4(dqgemm_format fmt_, const void* x, int M, int K, void* codes, void* scales,
                                       float* g_x, void* stream) {
-  const int fmt = storage_fmt((int)fmt_);
+  const int fmt = storage_fmt(internal_fmt((int)fmt_));
   if (fmt != FMT_MXFP4 && fmt != FMT_NVFP4) return DQ_ERR_UNSUPPORTED;
   const bool mx = fmt == FMT_MXFP4;
   if (!x || !codes || !scales || M < 1 || K < 1 || K % (mx ? 32 : 16) || (!mx && !g_x)) return DQ_ERR_INVALID_ARG;
@@ -938,7 +953,7 @@ dqgemm_status dqgemm_quantize_act_fp4(dqgemm_format fmt_, const void* x, int M, 
 
 dqgemm_status dqgemm_pack_host(dqgemm_format fmt_, const float* W, int K, int N, void* packed, void* scales,
                                float* global_scale) {
-  const int fmt = storage_fmt((int)fmt_);
+  const int fmt = storage_fmt(internal_fmt((int)fmt_));
   dqgemm_status st = check_shape(fmt, K, N);
   if (st != DQ_OK) return st;
   if (!W || !packed || !scales) return DQ_ERR_INVALID_ARG;
@@ -947,6 +962,10 @@ dqgemm_status dqgemm_pack_host(dqgemm_format fmt_, const float* W, int K, int N,
   for (size_t i = 0; i < count; ++i) {
     if (!std::isfinite(W[i])) return DQ_ERR_INVALID_ARG;
     amax = std::max(amax, std::fabs(W[i]));
+  }
+  if (fmt == FMT_FP8B) {
+    if (global_scale) *global_scale = 1.f;
+    return block_pack_host(W, K, N, packed, scales);
   }
   uint8_t* P = static_cast<uint8_t*>(packed);
   float g = 1.f;
@@ -999,11 +1018,19 @@ dqgemm_status dqgemm_pack_host(dqgemm_format fmt_, const float* W, int K, int N,
 
 dqgemm_status dqgemm_pack_device(dqgemm_format fmt_, const float* W, int K, int N, void* packed, void* scales,
                                  float* global_scale, void* stream) {
-  const int fmt = storage_fmt((int)fmt_);
+  const int fmt = storage_fmt(internal_fmt((int)fmt_));
   dqgemm_status st = check_shape(fmt, K, N);
   if (st != DQ_OK) return st;
   if (!W || !packed || !scales) return DQ_ERR_INVALID_ARG;
   if (!aligned16(W) || !aligned16(packed) || !aligned16(scales)) return DQ_ERR_ALIGNMENT;
+  if (fmt == FMT_FP8B) {
+    st = block_pack_device(W, K, N, packed, scales, static_cast<cudaStream_t>(stream));
+    if (st == DQ_OK && global_scale) {
+      st = cuda_err(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+      *global_scale = 1.f;
+    }
+    return st;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* P = static_cast<uint8_t*>(packed);
   const long long count = (long long)N * K;
@@ -1070,11 +1097,19 @@ float* noalloc_scratch(dqgemm_status* st) {
 
 dqgemm_status dqgemm_pack_device_noalloc(dqgemm_format fmt_, const float* W, int K, int N, void* packed,
                                          void* scales, float* global_scale, void* stream) {
-  const int fmt = storage_fmt((int)fmt_);
+  const int fmt = storage_fmt(internal_fmt((int)fmt_));
   dqgemm_status st = check_shape(fmt, K, N);
   if (st != DQ_OK) return st;
   if (!W || !packed || !scales) return DQ_ERR_INVALID_ARG;
   if (!aligned16(W) || !aligned16(packed) || !aligned16(scales)) return DQ_ERR_ALIGNMENT;
+  if (fmt == FMT_FP8B) {
+    st = block_pack_device(W, K, N, packed, scales, static_cast<cudaStream_t>(stream));
+    if (st == DQ_OK && global_scale) {
+      st = cuda_err(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+      *global_scale = 1.f;
+    }
+    return st;
+  }
   const long long count = (long long)N * K;
   const long long nparts = (count + kNoAllocChunk - 1) / kNoAllocChunk;
   if (fmt == FMT_NVFP4 && nparts > kNoAllocMaxPartials) return DQ_ERR_UNSUPPORTED;   // N*K > 2^28

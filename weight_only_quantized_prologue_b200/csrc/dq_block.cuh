@@ -1,0 +1,779 @@
+// dq_block.cuh -- products in e4m3 with a scale per 128 x 128 block of the
+// weight and per 128 activations of a row, dense or grouped by expert:
+//
+//   y[m, n] = sum_b sx[m, b] * sw[n / 128, b] * (sum_{k in block b} qx[m, k] qw[n, k])  + bias[n]
+//
+// The tensor core sums the 128 products of a block into a TMEM buffer of its
+// own (fp32); the epilogue warps multiply that partial by the block's two
+// scales and add it to their fp32 accumulators in registers while the next
+// block's MMAs run into another buffer.  Weights stay row-major [N, K]: TMA
+// writes the tensor core's swizzled image, so nothing is laid out again.
+//
+// Two kernels:
+//   block_skinny_kernel  y^T = W x^T: 128 weight rows are the MMA's M, BN
+//       activation rows its N (16..128).  Bound by the weight's bytes.  With
+//       few tiles the K range is split over a thread-block cluster, whose
+//       partials meet in distributed shared memory in rank order.
+//   block_pair_kernel    256 rows x 256 channels by a pair of CTAs
+//       (cta_group::2): each CTA holds 128 activation rows and half of the
+//       weight rows, so a product of 128 k costs each SM 32 KB of loads where
+//       a single CTA's 128 x 256 tile costs 48.  Bound by the tensor core.
+//
+// Grouped calls (E > 0 experts): rows offsets[e] .. offsets[e + 1] belong to
+// expert e.  The offsets are read on the device; each CTA counts the tiles
+// of every expert itself.  Offsets outside [0, M] are clamped, so no value in
+// them makes an access leave the buffers.
+#pragma once
+
+#include "dq_codec.h"
+#include "dq_common.cuh"
+
+namespace dq {
+
+constexpr int MAX_EXPERTS = 1024;
+
+struct BlockParams {
+  const float* sx;             // [M, kb]
+  const float* sw;             // [E][nb][kb]
+  const __nv_bfloat16* bias;   // [E][N] or null
+  __nv_bfloat16* y;            // [M, N]
+  const int* offsets;          // grouped: device [E + 1]
+  int* status;
+  int M, N, E;
+  int kb, nb;                  // blocks along K and N
+  int n_tiles, m_tiles;        // (m_tiles: dense)
+  int split;
+  int vec_y;                   // y rows are 16-byte aligned
+  unsigned long long timeout_ns, drain_ns;
+};
+
+// ---------------------------------------------------------------------------
+// tiles
+// ---------------------------------------------------------------------------
+struct BlockTile {
+  int e, n0;         // expert, first channel
+  int m0, m_end;     // first row, end of the expert's rows
+};
+
+__device__ __forceinline__ void expert_rows(const BlockParams& p, int e, int& a, int& b) {
+  a = max(0, min(p.M, p.offsets[e]));
+  b = max(a, min(p.M, p.offsets[e + 1]));
+}
+
+// start[e]: row tiles of the experts before e, start[E]: all of them.  The
+// whole CTA calls this (it ends with a barrier).
+template <int TM>
+__device__ __forceinline__ void count_tiles(const BlockParams& p, int* start) {
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    int a, b;
+    expert_rows(p, e, a, b);
+    start[e + 1] = (b - a + TM - 1) / TM;
+  }
+  if (threadIdx.x == 0) start[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int base = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + (int)threadIdx.x;
+      int v = e < p.E ? start[e + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if ((int)threadIdx.x >= o) v += u;
+      }
+      if (e < p.E) start[e + 1] = base + v;
+      base += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// tile t, rows fastest: neighbouring CTAs share a weight tile
+template <int TM, int TN, bool GROUPED>
+__device__ __forceinline__ BlockTile block_tile(const BlockParams& p, const int* start, int t) {
+  BlockTile r;
+  if constexpr (GROUPED) {
+    const int u = t / p.n_tiles;   // start[e] <= u < start[e + 1]
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    const int mt = start[lo + 1] - start[lo], local = t - start[lo] * p.n_tiles;
+    const int nt = local / mt;
+    int a, b;
+    expert_rows(p, lo, a, b);
+    r.e = lo;
+    r.n0 = nt * TN;
+    r.m0 = a + (local - nt * mt) * TM;
+    r.m_end = b;
+  } else {
+    const int nt = t / p.m_tiles;
+    r.e = 0;
+    r.n0 = nt * TN;
+    r.m0 = (t - nt * p.m_tiles) * TM;
+    r.m_end = p.M;
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// tensor memory reads whose wait carries the registers, so that no use of
+// them can be scheduled before it
+// ---------------------------------------------------------------------------
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float (&v)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "8, 16 or 32 columns");
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_wait_regs(float (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+               :
+               : "memory");
+  if constexpr (N > 8)
+    asm volatile("" : "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+  if constexpr (N > 16) {
+    asm volatile("" : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]));
+    asm volatile("" : "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+  }
+}
+
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// four consecutive blocks' scales of one row (0 past `end`)
+__device__ __forceinline__ void load_scales(const float* row, bool live, int b, int end, float (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = live && b + i < end ? row[b + i] : 0.f;
+}
+
+// ---------------------------------------------------------------------------
+// skinny: 128 channels x BN rows per CTA
+// warps: 0 weight copies, 1 MMA, 2 activation copies, 4..11 epilogue
+// ---------------------------------------------------------------------------
+template <int BN>
+struct SkinnyCfg {
+  static constexpr int W_BYTES = 128 * 128;
+  static constexpr int X_BYTES = BN * 128;
+  static constexpr int STAGE = W_BYTES + X_BYTES;          // both multiples of 1024
+  // two CTAs an SM up to 64 rows (also the next call's beside this one's),
+  // one at 128
+  static constexpr int ST = BN == 16 ? 5 : BN == 32 ? 5 : BN == 64 ? 4 : 6;
+  static constexpr int PB = 4;                             // partial buffers
+  static constexpr int TMEM_COLS = PB * BN < 32 ? 32 : PB * BN;
+  static constexpr int HALF = BN / 2;                      // columns per epilogue thread
+  static constexpr int BAR_OFF = ST * STAGE;
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int SC_OFF = BAR_OFF + BAR_BYTES;       // [8 warps][2][HALF] combined scales
+  static constexpr int SC_BYTES = 8 * 2 * HALF * 4;
+  static constexpr int TAB_OFF = SC_OFF + SC_BYTES;        // grouped: tile counts
+  static constexpr int TAB_BYTES = (MAX_EXPERTS + 1) * 4;
+  static constexpr int SMEM = TAB_OFF + TAB_BYTES + 1024;
+  static constexpr int CTAS = BN <= 64 ? 2 : 1;
+  static constexpr int THREADS = 384;
+  static_assert(X_BYTES % 1024 == 0, "swizzle atoms");
+  static_assert(BN * 128 * 4 <= ST * STAGE, "the reduction reuses the ring");
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
+  static_assert(CTAS * TMEM_COLS <= 512, "tensor memory");
+};
+
+template <int BN, bool GROUPED>
+__global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
+    block_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                        const BlockParams p) {
+  using C = SkinnyCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_w = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* full_x = full_w + C::ST;
+  uint64_t* empty = full_x + C::ST;          // stage read by the MMAs
+  uint64_t* acc_full = empty + C::ST;        // [PB]
+  uint64_t* acc_empty = acc_full + C::PB;    // [PB]
+  uint64_t* drain = acc_empty + C::PB;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);   // an epilogue warp gave up
+  static_assert((3 * C::ST + 2 * C::PB + 1) * 8 + 12 <= C::BAR_BYTES, "barriers");
+  int* start = reinterpret_cast<int*>(smem + C::TAB_OFF);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const auto ctl = [&] { return WaitCtl{abort_flag, p.status, p.timeout_ns}; };
+  const auto ctl_drain = [&] { return WaitCtl{nullptr, p.status, p.drain_ns}; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(&full_w[s], 1);
+      mbar_init(&full_x[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < C::PB; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *bad = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+
+  int tiles;
+  if constexpr (GROUPED) {
+    pdl_wait();   // the offsets may be the previous grid's output
+    count_tiles<BN>(p, start);
+    tiles = start[p.E] * p.n_tiles;
+  } else {
+    tiles = p.n_tiles * p.m_tiles;
+  }
+  // split-K: cluster c computes tile c, rank q its blocks [q kb / S, (q + 1) kb / S)
+  const int S = GROUPED ? 1 : p.split;
+  const int rank = S > 1 ? (int)cluster_rank() : 0;
+  const int t0 = S > 1 ? (int)blockIdx.x / S : (int)blockIdx.x;
+  const int step = S > 1 ? tiles : (int)gridDim.x;
+  const int b0 = rank * p.kb / S, b1 = (rank + 1) * p.kb / S;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ weight copies (ahead of the previous grid's end)
+    if (lane == 0) {
+      int it = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = t0; ok && t < tiles; t += step) {
+        const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
+        for (int b = b0; b < b1; ++b, ++it) {
+          if (it >= C::ST && !mbar_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
+          mbar_arrive_expect_tx(&full_w[s], C::W_BYTES);
+          tma_load_2d(smem + s * C::STAGE, &tmap_w, b * 128, tl.e * p.N + tl.n0, &full_w[s]);
+          if (++s == C::ST) { s = 0; ph ^= 1; }
+        }
+      }
+      for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) mbar_wait(&full_w[i % C::ST], (i / C::ST) & 1, ctl_drain());
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ activation copies
+    if (lane == 0) {
+      if constexpr (!GROUPED) pdl_wait();
+      int it = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = t0; ok && t < tiles; t += step) {
+        const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
+        for (int b = b0; b < b1; ++b, ++it) {
+          if (it >= C::ST && !mbar_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
+          mbar_arrive_expect_tx(&full_x[s], C::X_BYTES);
+          tma_load_2d(smem + s * C::STAGE + C::W_BYTES, &tmap_x, b * 128, tl.m0, &full_x[s]);
+          if (++s == C::ST) { s = 0; ph ^= 1; }
+        }
+      }
+      for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) mbar_wait(&full_x[i % C::ST], (i / C::ST) & 1, ctl_drain());
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      int s = 0, pb = 0;
+      uint32_t ph = 0, pph = 0;
+      bool ok = true, issued = false;
+      for (int t = t0; ok && t < tiles; t += step) {
+        for (int b = b0; b < b1; ++b) {
+          if (!mbar_wait(&acc_empty[pb], pph ^ 1, ctl()) || !mbar_wait(&full_w[s], ph, ctl()) ||
+              !mbar_wait(&full_x[s], ph, ctl())) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t wb = smem_u32(smem + s * C::STAGE), xb = wb + C::W_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8_ss(tmem + pb * BN, sdesc_sw128(wb + kk * 32), sdesc_sw128(xb + kk * 32), idesc_e4m3(BN), kk > 0 ? 1u : 0u);
+          issued = true;
+          tc_commit(&empty[s]);
+          tc_commit(&acc_full[pb]);
+          if (++s == C::ST) { s = 0; ph ^= 1; }
+          if (++pb == C::PB) { pb = 0; pph ^= 1; }
+        }
+      }
+      if (issued) {
+        tc_commit(drain);
+        mbar_wait(drain, 0, ctl_drain());
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ scaling, sum and output
+    if constexpr (!GROUPED) pdl_wait();
+    const int qd = warp & 3, h = (warp - 4) >> 2;
+    const int r = qd * 32 + lane;                       // channel within the tile
+    const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
+    float* sc = reinterpret_cast<float*>(smem + C::SC_OFF) + (warp - 4) * 2 * C::HALF;
+    constexpr int CPL = (C::HALF + 31) / 32;            // columns whose scales this lane fetches
+    constexpr int LD = C::HALF < 16 ? C::HALF : 16;
+    int pb = 0;
+    uint32_t pph = 0;
+    bool ok = true;
+    for (int t = t0; ok && t < tiles; t += step) {
+      const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
+      const float* sw = p.sw + ((size_t)tl.e * p.nb + (tl.n0 >> 7)) * p.kb;
+      const float* sxr[CPL];
+      bool live[CPL];
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) {
+        const int c = lane + 32 * j, m = tl.m0 + h * C::HALF + c;
+        live[j] = c < C::HALF && m < tl.m_end;
+        sxr[j] = p.sx + (size_t)(live[j] ? m : 0) * p.kb;
+      }
+      float nx[CPL][4], nw[4], cx[CPL][4], cw[4];
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) load_scales(sxr[j], live[j], b0, b1, nx[j]);
+      load_scales(sw, true, b0, b1, nw);
+      float acc[C::HALF];
+#pragma unroll
+      for (int i = 0; i < C::HALF; ++i) acc[i] = 0.f;
+      for (int bg = b0; ok && bg < b1; bg += 4) {
+        // this group's scales arrived while the last group was summed
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cw[i] = nw[i];
+#pragma unroll
+          for (int j = 0; j < CPL; ++j) cx[j][i] = nx[j][i];
+        }
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) load_scales(sxr[j], live[j], bg + 4, b1, nx[j]);
+        load_scales(sw, true, bg + 4, b1, nw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (bg + i >= b1) break;
+          float* buf = sc + (i & 1) * C::HALF;
+#pragma unroll
+          for (int j = 0; j < CPL; ++j)
+            if (lane + 32 * j < C::HALF) buf[lane + 32 * j] = cx[j][i] * cw[i];
+          __syncwarp();
+          if (!mbar_wait_warp(&acc_full[pb], pph, ctl())) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < C::HALF; c0 += LD) {
+            float v[LD];
+            tmem_ld_n<LD>(tmem + lane_base + pb * BN + h * C::HALF + c0, v);
+            tmem_wait_regs<LD>(v);
+#pragma unroll
+            for (int c = 0; c < LD; c += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(buf + c0 + c);
+              acc[c0 + c] = fmaf(v[c], f.x, acc[c0 + c]);
+              acc[c0 + c + 1] = fmaf(v[c + 1], f.y, acc[c0 + c + 1]);
+              acc[c0 + c + 2] = fmaf(v[c + 2], f.z, acc[c0 + c + 2]);
+              acc[c0 + c + 3] = fmaf(v[c + 3], f.w, acc[c0 + c + 3]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[pb]);
+          if (++pb == C::PB) { pb = 0; pph ^= 1; }
+        }
+      }
+      if (!ok) break;
+      if (S == 1) {
+        const int n = tl.n0 + r;
+        if (n < p.N) {
+          const float bias = p.bias ? __bfloat162float(p.bias[(size_t)tl.e * p.N + n]) : 0.f;
+#pragma unroll
+          for (int i = 0; i < C::HALF; ++i) {
+            const int m = tl.m0 + h * C::HALF + i;
+            if (m < tl.m_end) p.y[(size_t)m * p.N + n] = __float2bfloat16_rn(acc[i] + bias);
+          }
+        }
+      } else {
+        // every MMA of this CTA has completed: the ring is free for the partial [column][channel]
+        float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int i = 0; i < C::HALF; ++i) red[(h * C::HALF + i) * 128 + r] = acc[i];
+      }
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      *bad = 1;
+    }
+    __syncwarp();
+  }
+
+  if (S > 1) {
+    __syncwarp();
+    cluster_sync();   // every partial (or its absence) is in its CTA's shared memory
+    if (warp >= 4) {
+      const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t0);
+      const int cols = BN / S;                        // S is a power of two <= 8 <= BN
+      bool good = true;
+      for (int q = 0; q < S; ++q) good = good && ld_dsmem_u32(dsmem_addr(const_cast<uint32_t*>(bad), q)) == 0u;
+      if (good) {
+        for (int i = threadIdx.x - 128; i < cols * 128; i += 256) {
+          const int c = rank * cols + (i >> 7), n = tl.n0 + (i & 127), m = tl.m0 + c;
+          const float* cell = reinterpret_cast<const float*>(smem) + c * 128 + (i & 127);
+          float v = 0.f;
+          for (int q = 0; q < S; ++q) v += ld_dsmem_f32(dsmem_addr(cell, q));
+          if (n < p.N && m < tl.m_end) {
+            if (p.bias) v += __bfloat162float(p.bias[n]);
+            p.y[(size_t)m * p.N + n] = __float2bfloat16_rn(v);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while its shared memory is read
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------
+// pair: 256 rows x 256 channels by two CTAs
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {   // one warp of each CTA
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (256 rows over the pair) (+)= A . B^T, each CTA holding half of A's and of B's rows
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on the barrier of both CTAs when the MMAs issued so far are done
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+struct PairCfg {
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int ST = 6;
+  static constexpr int PB = 2;                  // partial buffers of 256 columns: all of TMEM
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int BAR_OFF = ST * STAGE;
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int TAB_OFF = BAR_OFF + BAR_BYTES;
+  static constexpr int SMEM = TAB_OFF + (MAX_EXPERTS + 1) * 4 + 1024;
+  static constexpr int THREADS = 384;
+  // M = 256, N = 256, e4m3 x e4m3 -> f32
+  static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+  // registers: 128 producer threads at 40, 256 epilogue threads at 216, out of
+  // the 384 x 168 of the launch
+  static constexpr int REGS_LOW = 40, REGS_HIGH = 216;
+  static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 160, "register split");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+template <bool GROUPED>
+__global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
+    block_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                      const BlockParams p) {
+  using C = PairCfg;
+  extern __shared__ uint8_t smem_raw[];
+  // (the same offset in both CTAs: the dynamic base is the same)
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);   // this CTA's copies of a stage have landed
+  uint64_t* peer_full = full + C::ST;        // leader: the other CTA's have
+  uint64_t* empty = peer_full + C::ST;       // both: the pair's MMAs have read the stage
+  uint64_t* acc_full = empty + C::ST;        // both
+  uint64_t* acc_empty = acc_full + C::PB;    // leader: the 8 + 8 epilogue warps have read a buffer
+  uint64_t* drain = acc_empty + C::PB;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((3 * C::ST + 2 * C::PB + 1) * 8 + 8 <= C::BAR_BYTES, "barriers");
+  int* start = reinterpret_cast<int*>(smem + C::TAB_OFF);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();   // 0: the leader, which issues the MMAs
+  const auto ctl = [&] { return WaitCtl{abort_flag, p.status, p.timeout_ns}; };
+  const auto ctl_drain = [&] { return WaitCtl{nullptr, p.status, p.drain_ns}; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&peer_full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < C::PB; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 16);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the other CTA's barriers are initialized
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+
+  int tiles;
+  if constexpr (GROUPED) {
+    pdl_wait();
+    count_tiles<256>(p, start);
+    tiles = start[p.E] * p.n_tiles;
+  } else {
+    tiles = p.n_tiles * p.m_tiles;
+  }
+  const int t0 = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_LOW));
+    if (warp == 0) {
+      // ---------------------------------------------------------- copies
+      if (lane == 0) {
+        if constexpr (!GROUPED) pdl_wait();
+        int it = 0, s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = t0; ok && t < tiles; t += step) {
+          const BlockTile tl = block_tile<256, 256, GROUPED>(p, start, t);
+          for (int b = 0; b < p.kb; ++b, ++it) {
+            if (it >= C::ST && !mbar_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
+            mbar_arrive_expect_tx(&full[s], C::STAGE);
+            tma_load_2d(smem + s * C::STAGE, &tmap_x, b * 128, tl.m0 + rank * 128, &full[s]);
+            tma_load_2d(smem + s * C::STAGE + C::A_BYTES, &tmap_w, b * 128, tl.e * p.N + tl.n0 + rank * 128, &full[s]);
+            if (++s == C::ST) { s = 0; ph ^= 1; }
+          }
+        }
+        for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) mbar_wait(&full[i % C::ST], (i / C::ST) & 1, ctl_drain());
+      }
+    } else if (warp == 2 && rank == 1) {
+      // ---------------------------------------------------------- tell the leader that this CTA's half has landed
+      if (lane == 0) {
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = t0; ok && t < tiles; t += step)
+          for (int b = 0; b < p.kb; ++b) {
+            if (!mbar_wait(&full[s], ph, ctl())) { ok = false; break; }
+            mbar_arrive_cluster(dsmem_addr(&peer_full[s], 0));
+            if (++s == C::ST) { s = 0; ph ^= 1; }
+          }
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---------------------------------------------------------- MMA
+      if (lane == 0) {
+        int s = 0, pb = 0;
+        uint32_t ph = 0, pph = 0;
+        bool ok = true, issued = false;
+        for (int t = t0; ok && t < tiles; t += step) {
+          for (int b = 0; b < p.kb; ++b) {
+            if (!mbar_wait_cluster(&acc_empty[pb], pph ^ 1, ctl()) || !mbar_wait(&full[s], ph, ctl()) ||
+                !mbar_wait_cluster(&peer_full[s], ph, ctl())) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t ab = smem_u32(smem + s * C::STAGE), bb = ab + C::A_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8_pair(tmem + pb * 256, sdesc_sw128(ab + kk * 32), sdesc_sw128(bb + kk * 32), C::IDESC, kk > 0 ? 1u : 0u);
+            issued = true;
+            tc_commit_pair(&empty[s]);
+            tc_commit_pair(&acc_full[pb]);
+            if (++s == C::ST) { s = 0; ph ^= 1; }
+            if (++pb == C::PB) { pb = 0; pph ^= 1; }
+          }
+        }
+        if (issued) {
+          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+                       : "memory");
+          mbar_wait(drain, 0, ctl_drain());
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ scaling, sum and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_HIGH));
+    if constexpr (!GROUPED) pdl_wait();
+    const int qd = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
+    const uint32_t empty_addr = dsmem_addr(acc_empty, 0);
+    int pb = 0;
+    uint32_t pph = 0;
+    bool ok = true;
+    for (int t = t0; ok && t < tiles; t += step) {
+      const BlockTile tl = block_tile<256, 256, GROUPED>(p, start, t);
+      const int m = tl.m0 + rank * 128 + qd * 32 + lane, n0 = tl.n0 + h * 128;
+      const bool live = m < tl.m_end;
+      const bool live_n = n0 < p.N;
+      const float* sxr = p.sx + (size_t)(live ? m : 0) * p.kb;
+      const float* sw = p.sw + ((size_t)tl.e * p.nb + (live_n ? n0 >> 7 : 0)) * p.kb;
+      float nx[4], nw[4], sc[4];
+      load_scales(sxr, live, 0, p.kb, nx);
+      load_scales(sw, live_n, 0, p.kb, nw);
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int bg = 0; ok && bg < p.kb; bg += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = nx[i] * nw[i];
+        load_scales(sxr, live, bg + 4, p.kb, nx);
+        load_scales(sw, live_n, bg + 4, p.kb, nw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (bg + i >= p.kb) break;
+          if (!mbar_wait_warp(&acc_full[pb], pph, ctl())) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ta = tmem + lane_base + pb * 256 + h * 128;
+#pragma unroll
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            float v[32];
+            tmem_ld_n<32>(ta + c0, v);
+            tmem_wait_regs<32>(v);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) acc[c0 + c] = fmaf(v[c], sc[i], acc[c0 + c]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(empty_addr + pb * 8);
+          if (++pb == C::PB) { pb = 0; pph ^= 1; }
+        }
+      }
+      if (!ok) break;
+      if (live && live_n) {
+        __nv_bfloat16* y = p.y + (size_t)m * p.N + n0;
+        const __nv_bfloat16* bias = p.bias ? p.bias + (size_t)tl.e * p.N + n0 : nullptr;
+        const int nn = p.N - n0;
+        if (p.vec_y && nn >= 128) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float a = acc[c + 2 * k], b = acc[c + 2 * k + 1];
+              if (bias) {
+                a += __bfloat162float(bias[c + 2 * k]);
+                b += __bfloat162float(bias[c + 2 * k + 1]);
+              }
+              const __nv_bfloat162 v2 = __floats2bfloat162_rn(a, b);
+              w[k] = *reinterpret_cast<const uint32_t*>(&v2);
+            }
+            *reinterpret_cast<uint4*>(y + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c < nn) y[c] = __float2bfloat16_rn(acc[c] + (bias ? __bfloat162float(bias[c]) : 0.f));
+        }
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  // both CTAs are done with each other's barriers, shared and tensor memory
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc_pair(tmem, C::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------
+// weight packing, checking and (debug) dequantization
+// ---------------------------------------------------------------------------
+
+// one CTA of 256 threads per 128 x 128 block of W fp32 [N, K]
+__global__ void __launch_bounds__(256) pack_fp8_block_kernel(const float* W, int N, int K, uint8_t* codes, float* scales) {
+  const int bn = blockIdx.y, bk = blockIdx.x;
+  const int rows = min(128, N - bn * 128), cols = min(128, K - bk * 128);
+  const float* w = W + (size_t)bn * 128 * K + bk * 128;
+  uint8_t* c = codes + (size_t)bn * 128 * K + bk * 128;
+  const int col = threadIdx.x & 127, r0 = threadIdx.x >> 7;
+  float a = 0.f;
+  if (col < cols)
+    for (int r = r0; r < rows; r += 2) a = fmaxf(a, fabsf(w[(size_t)r * K + col]));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+  __shared__ float wmax[8];
+  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, wmax[i]);
+  const float s = fdiv(a, 448.f);
+  if (threadIdx.x == 0) scales[(size_t)bn * gridDim.x + bk] = s;
+  if (col < cols)
+    for (int r = r0; r < rows; r += 2)
+      c[(size_t)r * K + col] = s > 0.f ? e4m3_encode_sat(fdiv(w[(size_t)r * K + col], s)) : 0;
+}
+
+// *flag becomes nonzero for a NaN code or a scale that is negative, infinite or NaN
+__global__ void check_fp8_block_kernel(const uint8_t* codes, size_t count, const float* scales, size_t ns, int* flag) {
+  int bad = 0;
+  const size_t i0 = blockIdx.x * (size_t)blockDim.x + threadIdx.x, step = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = i0; i < count / 16; i += step) {
+    const uint4 v = reinterpret_cast<const uint4*>(codes)[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)   // a byte of 0x7F or 0xFF: its low 7 bits all set
+      bad |= ((((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u) ? 1 : 0;
+  }
+  for (size_t i = i0; i < ns; i += step) bad |= (scales[i] >= 0.f && scales[i] <= 3.402823466e38f) ? 0 : 2;
+  if (bad) *reinterpret_cast<volatile int*>(flag) = bad;   // (any writer's value refuses the weight)
+}
+
+__global__ void dequant_fp8_block_kernel(const uint8_t* codes, const float* scales, size_t rows, int N, int K,
+                                         __nv_bfloat16* out) {
+  const int kb = (K + 127) / 128, nb = (N + 127) / 128;
+  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < rows * K; i += (size_t)gridDim.x * blockDim.x) {
+    const size_t row = i / K;
+    const int k = (int)(i - row * K), e = (int)(row / N), n = (int)(row - (size_t)e * N);
+    const float s = scales[((size_t)e * nb + n / 128) * kb + k / 128];
+    out[i] = __float2bfloat16_rn(__fmul_rn(e4m3_decode(codes[i]), s));
+  }
+}
+
+}  // namespace dq

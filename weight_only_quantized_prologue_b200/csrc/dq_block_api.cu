@@ -1,0 +1,383 @@
+// dq_block_api.cu -- block-scaled FP8 layers and experts: handles, launch plan
+// and the entry points of include/dqgemm.h that only they have.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "dq_block.cuh"
+#include "dq_handle.h"
+
+using namespace dq;
+
+namespace {
+
+constexpr int QB = 128;   // elements per scale
+
+int blocks(int n) { return (n + QB - 1) / QB; }
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+struct BlockPlan {
+  bool pair;       // block_pair_kernel, else block_skinny_kernel
+  int bn;          // rows per tile
+  int m_tiles, n_tiles;
+  int split;
+  int grid;        // CTAs
+};
+
+template <int BN>
+struct Skinny {
+  using C = SkinnyCfg<BN>;
+  template <bool G>
+  static cudaError_t attr() {
+    cudaError_t e = cudaFuncSetAttribute(block_skinny_kernel<BN, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(block_skinny_kernel<BN, G>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               (int)cudaSharedmemCarveoutMaxShared);
+    return e;
+  }
+};
+
+template <bool G>
+cudaError_t pair_attr() {
+  cudaError_t e = cudaFuncSetAttribute(block_pair_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(block_pair_kernel<G>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared);
+  return e;
+}
+
+cudaError_t set_attrs() {
+  cudaError_t e = cudaSuccess;
+  for (cudaError_t r : {Skinny<16>::attr<false>(), Skinny<32>::attr<false>(), Skinny<64>::attr<false>(),
+                        Skinny<128>::attr<false>(), Skinny<16>::attr<true>(), Skinny<32>::attr<true>(),
+                        Skinny<64>::attr<true>(), Skinny<128>::attr<true>(), pair_attr<false>(), pair_attr<true>()})
+    if (e == cudaSuccess) e = r;
+  return e;
+}
+
+int ctas_per_sm(int bn) { return bn <= 64 ? 2 : 1; }
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// the largest power of two S <= 8, S <= kb, with T * S CTAs resident at once
+int pick_split(const dqgemm_s* h, long long T, int bn) {
+  const long long slots = (long long)h->num_sms * ctas_per_sm(bn);
+  int s = 1;
+  while (s < 8 && 2 * s <= h->k_stages && T * 2 * s <= slots) s *= 2;
+  return s;
+}
+
+BlockPlan dense_plan(const dqgemm_s* h, int M) {
+  BlockPlan pl{};
+  pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  if (M > 64) {
+    const long long t1 = ceil_div(M, 128) * h->n_tiles, t2 = ceil_div(M, 256) * ceil_div(h->N, 256);
+    const int s = pick_split(h, t1, 128);
+    const long long c1 = ceil_div(t1 * s, h->num_sms) * ceil_div(h->k_stages, s) * 520;
+    const long long c2 = ceil_div(t2, h->num_sms / 2) * h->k_stages * 600;
+    if (c2 <= c1) {
+      pl.pair = true;
+      pl.bn = 256;
+    }
+  }
+  pl.m_tiles = (int)ceil_div(M, pl.bn);
+  pl.n_tiles = (int)ceil_div(h->N, pl.pair ? 256 : 128);
+  const long long T = (long long)pl.m_tiles * pl.n_tiles;
+  if (pl.pair) {
+    pl.split = 1;
+    pl.grid = 2 * (int)std::min<long long>(T, h->num_sms / 2);
+  } else {
+    pl.split = pick_split(h, T, pl.bn);
+    pl.grid = (int)std::min<long long>(T * pl.split, pl.split > 1 ? T * pl.split : (long long)h->num_sms * ctas_per_sm(pl.bn));
+  }
+  return pl;
+}
+
+// The rows of each expert are known on the device only; the tile is picked
+// by their mean.
+BlockPlan grouped_plan(const dqgemm_s* h, int M) {
+  BlockPlan pl{};
+  const long long mean = ceil_div(M, h->E);
+  pl.pair = mean > 160;
+  pl.bn = pl.pair ? 256 : M <= 16 ? 16 : mean <= 16 ? 32 : mean <= 48 ? 64 : 128;
+  pl.n_tiles = (int)ceil_div(h->N, pl.pair ? 256 : 128);
+  pl.m_tiles = 0;
+  pl.split = 1;
+  // at most one partial row tile per expert with rows
+  const long long T = (M / pl.bn + std::min(h->E, M)) * (long long)pl.n_tiles;
+  pl.grid = pl.pair ? 2 * (int)std::min<long long>(T, h->num_sms / 2)
+                    : (int)std::min<long long>(T, (long long)h->num_sms * ctas_per_sm(pl.bn));
+  return pl;
+}
+
+// ---------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------
+
+// the map of the codes q [M, K] in boxes of 128 k x `rows` rows, encoded once
+// for a buffer that comes again
+bool codes_map(dqgemm_s* h, const void* q, int M, int rows, CUtensorMap* tm) {
+  std::lock_guard<std::mutex> lock(h->maps_mu);
+  for (const auto& e : h->maps) {
+    if (e.x == q && e.M == M && e.bn == rows) {
+      *tm = e.map;
+      return true;
+    }
+  }
+  if (!make_q_map(tm, q, M, h->K, rows)) return false;
+  auto& e = h->maps[h->next_map];
+  h->next_map = (h->next_map + 1) % dqgemm_s::kMaps;
+  e.x = q;
+  e.M = M;
+  e.bn = rows;
+  e.xq = true;
+  e.map = *tm;
+  return true;
+}
+
+template <typename K>
+cudaError_t launch(K kern, int grid, int threads, int smem, int cluster, const CUtensorMap& tw, const CUtensorMap& tx,
+                   const BlockParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute a[2];
+  int na = 0;
+  if (pdl_enabled()) {
+    a[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
+  if (cluster > 1) {
+    a[na].id = cudaLaunchAttributeClusterDimension;
+    a[na].val.clusterDim.x = cluster;
+    a[na].val.clusterDim.y = 1;
+    a[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  cfg.attrs = a;
+  cfg.numAttrs = na;
+  return cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
+}
+
+template <bool G>
+cudaError_t launch_plan(const BlockPlan& pl, const CUtensorMap& tw, const CUtensorMap& tx, const BlockParams& p,
+                        cudaStream_t s) {
+  // (the pair kernel's cluster size is a property of the kernel)
+  if (pl.pair) return launch(block_pair_kernel<G>, pl.grid, PairCfg::THREADS, PairCfg::SMEM, 1, tw, tx, p, s);
+  switch (pl.bn) {
+    case 16: return launch(block_skinny_kernel<16, G>, pl.grid, 384, SkinnyCfg<16>::SMEM, pl.split, tw, tx, p, s);
+    case 32: return launch(block_skinny_kernel<32, G>, pl.grid, 384, SkinnyCfg<32>::SMEM, pl.split, tw, tx, p, s);
+    case 64: return launch(block_skinny_kernel<64, G>, pl.grid, 384, SkinnyCfg<64>::SMEM, pl.split, tw, tx, p, s);
+    default: return launch(block_skinny_kernel<128, G>, pl.grid, 384, SkinnyCfg<128>::SMEM, pl.split, tw, tx, p, s);
+  }
+}
+
+// arguments checked by the callers
+dqgemm_status run_codes(dqgemm_handle h, const void* q, const float* sx, int M, const int* offsets, void* y, void* stream) {
+  const BlockPlan pl = offsets ? grouped_plan(h, M) : dense_plan(h, M);
+  if ((M / pl.bn + (long long)std::max(h->E, 1)) * pl.n_tiles > 0x7FFFFFFFll) return DQ_ERR_UNSUPPORTED;
+  CUtensorMap tx;
+  if (!codes_map(h, q, M, pl.pair ? 128 : pl.bn, &tx)) return DQ_ERR_CUDA;
+  BlockParams p{};
+  p.sx = sx;
+  p.sw = h->col_scale;
+  p.bias = h->bias;
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.offsets = offsets;
+  p.status = h->status;
+  p.M = M;
+  p.N = h->N;
+  p.E = h->E;
+  p.kb = h->k_stages;
+  p.nb = h->n_tiles;
+  p.n_tiles = pl.n_tiles;
+  p.m_tiles = pl.m_tiles;
+  p.split = pl.split;
+  p.vec_y = h->N % 8 == 0 && aligned16(y);
+  p.timeout_ns = h->timeout_ns;
+  p.drain_ns = std::max(timeout_ns(), kDefaultTimeoutNs);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_err(offsets ? launch_plan<true>(pl, h->wmap, tx, p, s) : launch_plan<false>(pl, h->wmap, tx, p, s));
+}
+
+}  // namespace
+
+namespace dq {
+
+dqgemm_status block_create(dqgemm_handle* out, int E, int K, int N, const void* packed_w, const void* scales,
+                           const void* bias) {
+  // (out set to null and the shape checked by the callers)
+  if (!packed_w || !scales) return DQ_ERR_INVALID_ARG;
+  if (!aligned16(packed_w) || !aligned16(scales) || (bias && !aligned16(bias))) return DQ_ERR_ALIGNMENT;
+  if (!is_device_ptr(packed_w) || !is_device_ptr(scales) || (bias && !is_device_ptr(bias))) return DQ_ERR_INVALID_ARG;
+  if ((long long)E * N > 0x7FFFFFFFll - 256) return DQ_ERR_UNSUPPORTED;   // (a row index of the weight's tensor map)
+  dqgemm_s* h = new (std::nothrow) dqgemm_s();
+  if (!h) return DQ_ERR_ALLOC;
+  h->fmt = FMT_FP8B;
+  h->K = K;
+  h->N = N;
+  h->E = E;
+  h->k_stages = blocks(K);
+  h->n_tiles = blocks(N);
+  h->timeout_ns = timeout_ns();
+  cudaGetDevice(&h->device);
+  cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
+  const size_t rows = (size_t)E * N, wb = rows * K, ns = (size_t)E * h->n_tiles * h->k_stages;
+  h->wchunk_bytes = wb;
+  h->weight_bytes = (long long)(wb + ns * 4);
+  cudaError_t e = cudaMalloc(&h->wchunks, wb);
+  if (e == cudaSuccess) e = cudaMalloc(&h->col_scale, ns * 4);
+  if (e == cudaSuccess && bias) e = cudaMalloc(&h->bias, rows * 2);
+  if (e == cudaSuccess) e = cudaHostAlloc(&h->status_host, sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    dqgemm_destroy(h);
+    return DQ_ERR_ALLOC;
+  }
+  *h->status_host = 0;
+  e = cudaHostGetDevicePointer(reinterpret_cast<void**>(&h->status), h->status_host, 0);
+  // codes and scales the GPU finds outside the format are counted in the status word
+  if (e == cudaSuccess) e = cudaMemcpy(h->wchunks, packed_w, wb, cudaMemcpyDeviceToDevice);
+  if (e == cudaSuccess) e = cudaMemcpy(h->col_scale, scales, ns * 4, cudaMemcpyDeviceToDevice);
+  if (e == cudaSuccess && bias) e = cudaMemcpy(h->bias, bias, rows * 2, cudaMemcpyDeviceToDevice);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) {
+    check_fp8_block_kernel<<<h->num_sms * 4, 256>>>(h->wchunks, wb, h->col_scale, ns, h->status);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = set_attrs();
+  if (e != cudaSuccess || !make_q_map(&h->wmap, h->wchunks, (int)rows, K, 128)) {
+    dqgemm_destroy(h);
+    return DQ_ERR_CUDA;
+  }
+  if (*h->status_host != 0) {
+    dqgemm_destroy(h);
+    return DQ_ERR_INVALID_ARG;
+  }
+  *out = h;
+  return DQ_OK;
+}
+
+// x bf16: quantized into the handle's workspace (codes, then scales), then the product
+dqgemm_status block_run_x(dqgemm_handle h, const void* x, int M, void* y, void* stream) {
+  if (!aligned16(x) || !aligned16(y)) return DQ_ERR_ALIGNMENT;
+  const size_t qb = ((size_t)M * h->K + 255) / 256 * 256, total = qb + (size_t)M * h->k_stages * 4;
+  {
+    std::lock_guard<std::mutex> lock(h->maps_mu);
+    if (h->ws_bytes < total) {
+      // grow: calls already launched may still read the old workspace
+      if (cudaDeviceSynchronize() != cudaSuccess) return DQ_ERR_CUDA;
+      cudaFree(h->ws);
+      h->ws = nullptr;
+      h->ws_bytes = 0;
+      for (auto& m : h->maps) m.x = nullptr;
+      if (cudaMalloc(&h->ws, total) != cudaSuccess) {
+        cudaGetLastError();
+        h->ws = nullptr;
+        return DQ_ERR_ALLOC;
+      }
+      h->ws_bytes = total;
+    }
+  }
+  float* sx = reinterpret_cast<float*>(h->ws + qb);
+  const dqgemm_status st = dqgemm_quantize_act_fp8_block(DQ_BF16, x, h->K, M, h->K, h->ws, sx, stream);
+  return st == DQ_OK ? run_codes(h, h->ws, sx, M, nullptr, y, stream) : st;
+}
+
+dqgemm_status block_dequantize(dqgemm_handle h, void* w_bf16, void* stream) {
+  dequant_fp8_block_kernel<<<h->num_sms * 8, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      h->wchunks, h->col_scale, (size_t)h->E * h->N, h->N, h->K, static_cast<__nv_bfloat16*>(w_bf16));
+  return cuda_err(cudaGetLastError());
+}
+
+void block_fill_plan(dqgemm_handle h, int M, dqgemm_plan* pl) {
+  std::memset(pl, 0, sizeof(*pl));
+  const BlockPlan b = h->E > 1 ? grouped_plan(h, M) : dense_plan(h, M);
+  pl->bn = b.bn;
+  pl->m_tiles = (int)ceil_div(M, b.bn);
+  pl->n_tiles = b.n_tiles;
+  pl->k_stages = h->k_stages;
+  pl->grid = b.grid;
+  pl->max_segments = b.split;
+  pl->stages = pl->x_stages = b.pair ? PairCfg::ST
+                              : b.bn == 16 ? SkinnyCfg<16>::ST
+                              : b.bn == 32 ? SkinnyCfg<32>::ST
+                              : b.bn == 64 ? SkinnyCfg<64>::ST
+                                           : SkinnyCfg<128>::ST;
+  pl->smem_bytes = b.pair ? PairCfg::SMEM
+                   : b.bn == 16 ? SkinnyCfg<16>::SMEM
+                   : b.bn == 32 ? SkinnyCfg<32>::SMEM
+                   : b.bn == 64 ? SkinnyCfg<64>::SMEM
+                                : SkinnyCfg<128>::SMEM;
+  pl->workspace_bytes = h->E > 1 ? 0 : ((long long)M * h->K + 255) / 256 * 256 + (long long)M * h->k_stages * 4;
+  pl->weight_bytes = h->weight_bytes;
+  const long long T = (long long)pl->m_tiles * b.n_tiles;
+  const long long at_once = b.pair ? b.grid / 2 : b.grid;
+  pl->max_cta_stages = b.split > 1 ? (int)ceil_div(h->k_stages, b.split) : (int)ceil_div(T, at_once) * h->k_stages;
+}
+
+dqgemm_status block_pack_host(const float* W, int K, int N, void* packed, void* scales) {
+  uint8_t* P = static_cast<uint8_t*>(packed);
+  float* S = static_cast<float*>(scales);
+  for (int i = 0; i < blocks(N); ++i)
+    for (int j = 0; j < blocks(K); ++j) {
+      const int n1 = std::min(N, (i + 1) * QB), k1 = std::min(K, (j + 1) * QB);
+      float a = 0.f;
+      for (int n = i * QB; n < n1; ++n)
+        for (int k = j * QB; k < k1; ++k) a = std::max(a, std::fabs(W[(size_t)n * K + k]));
+      const float s = fdiv(a, 448.f);
+      S[(size_t)i * blocks(K) + j] = s;
+      for (int n = i * QB; n < n1; ++n)
+        for (int k = j * QB; k < k1; ++k)
+          P[(size_t)n * K + k] = s > 0.f ? e4m3_encode_sat(fdiv(W[(size_t)n * K + k], s)) : 0;
+    }
+  return DQ_OK;
+}
+
+dqgemm_status block_pack_device(const float* W, int K, int N, void* packed, void* scales, cudaStream_t s) {
+  if (blocks(N) > 65535) return DQ_ERR_UNSUPPORTED;   // a grid row per block of channels
+  pack_fp8_block_kernel<<<dim3(blocks(K), blocks(N)), 256, 0, s>>>(W, N, K, static_cast<uint8_t*>(packed),
+                                                                   static_cast<float*>(scales));
+  return cuda_err(cudaGetLastError());
+}
+
+}  // namespace dq
+
+extern "C" {
+
+dqgemm_status dqgemm_create_experts(dqgemm_handle* out, dqgemm_format fmt, int E, int K, int N, const void* packed_w,
+                                    const void* scales, const void* bias) {
+  if (!out) return DQ_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (E < 1 || K < 1 || N < 1 || (int)fmt < 0 || (int)fmt > (int)DQ_FP8_BLOCK128) return DQ_ERR_INVALID_ARG;
+  if (fmt != DQ_FP8_BLOCK128 || E > MAX_EXPERTS) return DQ_ERR_UNSUPPORTED;
+  if (K % 16) return DQ_ERR_INVALID_ARG;
+  return block_create(out, E, K, N, packed_w, scales, bias);
+}
+
+dqgemm_status dqgemm_run_fp8_block_quantized(dqgemm_handle h, const void* q, const float* scales, int M, void* y,
+                                             void* stream) {
+  if (!h || !q || !scales || !y || M < 1) return DQ_ERR_INVALID_ARG;
+  if (h->fmt != FMT_FP8B || h->E != 1) return DQ_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(y) || reinterpret_cast<uintptr_t>(scales) % 4) return DQ_ERR_ALIGNMENT;
+  return run_codes(h, q, scales, M, nullptr, y, stream);
+}
+
+dqgemm_status dqgemm_run_experts_quantized(dqgemm_handle h, const void* q, const float* scales, int M, const int* offsets,
+                                           void* y, void* stream) {
+  if (!h || !q || !scales || !offsets || !y || M < 1) return DQ_ERR_INVALID_ARG;
+  if (h->fmt != FMT_FP8B) return DQ_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(y) || reinterpret_cast<uintptr_t>(scales) % 4 ||
+      reinterpret_cast<uintptr_t>(offsets) % 4)
+    return DQ_ERR_ALIGNMENT;
+  return run_codes(h, q, scales, M, offsets, y, stream);
+}
+
+}  // extern "C"

@@ -43,10 +43,28 @@ struct dqgemm_s {
   static constexpr int kMaps = 8;
   MapEntry maps[kMaps];
   int next_map = 0;
+  // block-scaled FP8 (fmt == FMT_FP8B): wchunks holds the canonical codes
+  // [E * N, K], col_scale the block scales [E][N / 128][K / 128] (rounded up)
+  int E = 1;
+  CUtensorMap wmap;                 // boxes of 128 k x 128 rows of the codes
   std::mutex maps_mu;               // run entry points may be called from several threads
 };
 
 namespace dq {
+
+// the handle's fmt of a block-scaled FP8 layer (the public DQ_FP8_BLOCK128;
+// 8 and 9 name kernel variants here)
+constexpr int FMT_FP8B = 10;
+
+// block-scaled FP8 (dq_block_api.cu); arguments checked by the callers where
+// a comment says so
+dqgemm_status block_create(dqgemm_handle* out, int E, int K, int N, const void* packed_w, const void* scales,
+                           const void* bias);
+dqgemm_status block_run_x(dqgemm_handle h, const void* x, int M, void* y, void* stream);
+dqgemm_status block_dequantize(dqgemm_handle h, void* w_bf16, void* stream);
+void block_fill_plan(dqgemm_handle h, int M, dqgemm_plan* plan);
+dqgemm_status block_pack_host(const float* W, int K, int N, void* packed, void* scales);      // W finite
+dqgemm_status block_pack_device(const float* W, int K, int N, void* packed, void* scales, cudaStream_t s);
 
 constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;   // 2 s
 
