@@ -17,7 +17,9 @@
 //   block_pair_kernel    256 rows x 256 channels by a pair of CTAs
 //       (cta_group::2): each CTA holds 128 activation rows and half of the
 //       weight rows, so a product of 128 k costs each SM 32 KB of loads where
-//       a single CTA's 128 x 256 tile costs 48.  Bound by the tensor core.
+//       a single CTA's 128 x 256 tile costs 48.  The two halves of 128
+//       channels are separate chains (MMA thread, partial buffers, epilogue
+//       warps), so one half's MMAs run while the other's partial is read.
 //
 // Grouped calls (E > 0 experts): rows offsets[e] .. offsets[e + 1] belong to
 // expert e.  The offsets are read on the device; each CTA counts the tiles
@@ -116,6 +118,67 @@ __device__ __forceinline__ BlockTile block_tile(const BlockParams& p, const int*
     r.m_end = p.M;
   }
   return r;
+}
+
+// One lane of a converged warp, the same each time.  The MMAs and copies are
+// issued under this and not under a test of the lane: they take their
+// descriptors from uniform registers, and the compiler knows of elect.sync
+// that one thread runs (of lane == 0 it does not, and wraps each instruction
+// in a loop over the active lanes).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// ---------------------------------------------------------------------------
+// bounded waits without a clock on the common path: the limit is looked at
+// only after a round of tries (reading the global timer first costs every
+// wait that does not succeed at once several hundred cycles, which the MMA
+// thread and the epilogue pay for each block of K).  try_wait suspends the
+// thread for a short time of the hardware's choosing.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, const WaitCtl ctl) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (int round = 0;; ++round) {
+    if (round > 0 || ctl.timeout_ns < 1000u) {
+      if (t0 == 0) t0 = globaltimer_ns();
+      if (wait_give_up(ctl, t0)) return false;
+    }
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+  }
+}
+// whether three barriers have all completed their phases, looked at together
+__device__ __forceinline__ bool mbar_try_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+      "and.pred p, p, q;\n\t"
+      "and.pred p, p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb), "r"(smem_u32(c)), "r"(pc)
+      : "memory");
+  return ok != 0;
+}
+// the whole warp: every lane observes the phase itself
+__device__ __forceinline__ bool block_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtl ctl) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = block_wait(bar, parity, ctl) ? 1 : 0;
+  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  if (ok) mbar_try_wait(bar, parity);
+  return ok != 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -273,25 +336,25 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
 
   if (warp == 0) {
     // ------------------------------------------------------------ weight copies (ahead of the previous grid's end)
-    if (lane == 0) {
+    if (elect_one()) {
       int it = 0, s = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = t0; ok && t < tiles; t += step) {
         const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
         for (int b = b0; b < b1; ++b, ++it) {
-          if (it >= C::ST && !mbar_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
+          if (it >= C::ST && !block_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
           mbar_arrive_expect_tx(&full_w[s], C::W_BYTES);
           tma_load_2d(smem + s * C::STAGE, &tmap_w, b * 128, tl.e * p.N + tl.n0, &full_w[s]);
           if (++s == C::ST) { s = 0; ph ^= 1; }
         }
       }
-      for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) mbar_wait(&full_w[i % C::ST], (i / C::ST) & 1, ctl_drain());
+      for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) block_wait(&full_w[i % C::ST], (i / C::ST) & 1, ctl_drain());
     }
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ activation copies
-    if (lane == 0) {
+    if (elect_one()) {
       if constexpr (!GROUPED) pdl_wait();
       int it = 0, s = 0;
       uint32_t ph = 0;
@@ -299,25 +362,25 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
       for (int t = t0; ok && t < tiles; t += step) {
         const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
         for (int b = b0; b < b1; ++b, ++it) {
-          if (it >= C::ST && !mbar_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
+          if (it >= C::ST && !block_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
           mbar_arrive_expect_tx(&full_x[s], C::X_BYTES);
           tma_load_2d(smem + s * C::STAGE + C::W_BYTES, &tmap_x, b * 128, tl.m0, &full_x[s]);
           if (++s == C::ST) { s = 0; ph ^= 1; }
         }
       }
-      for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) mbar_wait(&full_x[i % C::ST], (i / C::ST) & 1, ctl_drain());
+      for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) block_wait(&full_x[i % C::ST], (i / C::ST) & 1, ctl_drain());
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0, pb = 0;
       uint32_t ph = 0, pph = 0;
       bool ok = true, issued = false;
       for (int t = t0; ok && t < tiles; t += step) {
         for (int b = b0; b < b1; ++b) {
-          if (!mbar_wait(&acc_empty[pb], pph ^ 1, ctl()) || !mbar_wait(&full_w[s], ph, ctl()) ||
-              !mbar_wait(&full_x[s], ph, ctl())) { ok = false; break; }
+          if (!block_wait(&acc_empty[pb], pph ^ 1, ctl()) || !block_wait(&full_w[s], ph, ctl()) ||
+              !block_wait(&full_x[s], ph, ctl())) { ok = false; break; }
           tc_fence_after();
           const uint32_t wb = smem_u32(smem + s * C::STAGE), xb = wb + C::W_BYTES;
 #pragma unroll
@@ -332,7 +395,7 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
       }
       if (issued) {
         tc_commit(drain);
-        mbar_wait(drain, 0, ctl_drain());
+        block_wait(drain, 0, ctl_drain());
       }
     }
     __syncwarp();
@@ -385,7 +448,7 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
           for (int j = 0; j < CPL; ++j)
             if (lane + 32 * j < C::HALF) buf[lane + 32 * j] = cx[j][i] * cw[i];
           __syncwarp();
-          if (!mbar_wait_warp(&acc_full[pb], pph, ctl())) { ok = false; break; }
+          if (!block_wait_warp(&acc_full[pb], pph, ctl())) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
           for (int c0 = 0; c0 < C::HALF; c0 += LD) {
@@ -492,24 +555,28 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 struct PairCfg {
   static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int ST = 6;
-  static constexpr int PB = 2;                  // partial buffers of 256 columns: all of TMEM
+  static constexpr int ST = 5;
+  static constexpr int PB = 2;                  // partial buffers of 2 x 128 columns: all of TMEM
   static constexpr int TMEM_COLS = 512;
   static constexpr int BAR_OFF = ST * STAGE;
   static constexpr int BAR_BYTES = 256;
-  static constexpr int TAB_OFF = BAR_OFF + BAR_BYTES;
+  // output staging: per epilogue warp 32 rows of 32 bf16, rows 80 bytes apart
+  // (16-byte pieces of 8 neighbouring rows then lie in different banks)
+  static constexpr int OUT_PITCH = 80;
+  static constexpr int OUT_OFF = BAR_OFF + BAR_BYTES;
+  static constexpr int OUT_BYTES = 8 * 32 * OUT_PITCH;
+  static constexpr int TAB_OFF = OUT_OFF + OUT_BYTES;
   static constexpr int SMEM = TAB_OFF + (MAX_EXPERTS + 1) * 4 + 1024;
-  static constexpr int THREADS = 384;
+  static constexpr int THREADS = 384;   // 4 warps of copies and MMAs, 8 of sums
   // M = 256, N = 256, e4m3 x e4m3 -> f32
-  static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-  // registers: 128 producer threads at 40, 256 epilogue threads at 216, out of
-  // the 384 x 168 of the launch
+  static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+  // registers: 128 threads at 40, 256 at 216, out of the launch's 384 x 168
   static constexpr int REGS_LOW = 40, REGS_HIGH = 216;
   static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 160, "register split");
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -527,11 +594,11 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
   uint64_t* peer_full = full + C::ST;        // leader: the other CTA's have
   uint64_t* empty = peer_full + C::ST;       // both: the pair's MMAs have read the stage
   uint64_t* acc_full = empty + C::ST;        // both
-  uint64_t* acc_empty = acc_full + C::PB;    // leader: the 8 + 8 epilogue warps have read a buffer
-  uint64_t* drain = acc_empty + C::PB;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* acc_empty = acc_full + 2 * C::PB;    // leader: the 8 + 8 epilogue warps have read a buffer
+  uint64_t* drain = acc_empty + 2 * C::PB;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((3 * C::ST + 2 * C::PB + 1) * 8 + 8 <= C::BAR_BYTES, "barriers");
+  static_assert((3 * C::ST + 4 * C::PB + 2) * 8 + 8 <= C::BAR_BYTES, "barriers");
   int* start = reinterpret_cast<int*>(smem + C::TAB_OFF);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -543,13 +610,14 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&peer_full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);
     }
-    for (int b = 0; b < C::PB; ++b) {
+    for (int b = 0; b < 2 * C::PB; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 16);
+      mbar_init(&acc_empty[b], 8);   // 4 warps of each CTA
     }
     mbar_init(drain, 1);
+    mbar_init(drain + 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -575,7 +643,7 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_LOW));
     if (warp == 0) {
       // ---------------------------------------------------------- copies
-      if (lane == 0) {
+      if (elect_one()) {
         if constexpr (!GROUPED) pdl_wait();
         int it = 0, s = 0;
         uint32_t ph = 0;
@@ -583,54 +651,58 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
         for (int t = t0; ok && t < tiles; t += step) {
           const BlockTile tl = block_tile<256, 256, GROUPED>(p, start, t);
           for (int b = 0; b < p.kb; ++b, ++it) {
-            if (it >= C::ST && !mbar_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
+            if (it >= C::ST && !block_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
             mbar_arrive_expect_tx(&full[s], C::STAGE);
             tma_load_2d(smem + s * C::STAGE, &tmap_x, b * 128, tl.m0 + rank * 128, &full[s]);
-            tma_load_2d(smem + s * C::STAGE + C::A_BYTES, &tmap_w, b * 128, tl.e * p.N + tl.n0 + rank * 128, &full[s]);
+            tma_load_2d(smem + s * C::STAGE + C::A_BYTES, &tmap_w, b * 128, tl.e * p.N + tl.n0 + rank * 64, &full[s]);
+            tma_load_2d(smem + s * C::STAGE + C::A_BYTES + 8192, &tmap_w, b * 128, tl.e * p.N + tl.n0 + 128 + rank * 64, &full[s]);
             if (++s == C::ST) { s = 0; ph ^= 1; }
           }
         }
-        for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) mbar_wait(&full[i % C::ST], (i / C::ST) & 1, ctl_drain());
+        for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) block_wait(&full[i % C::ST], (i / C::ST) & 1, ctl_drain());
       }
     } else if (warp == 2 && rank == 1) {
       // ---------------------------------------------------------- tell the leader that this CTA's half has landed
-      if (lane == 0) {
+      if (elect_one()) {
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
         for (int t = t0; ok && t < tiles; t += step)
           for (int b = 0; b < p.kb; ++b) {
-            if (!mbar_wait(&full[s], ph, ctl())) { ok = false; break; }
+            if (!block_wait(&full[s], ph, ctl())) { ok = false; break; }
             mbar_arrive_cluster(dsmem_addr(&peer_full[s], 0));
             if (++s == C::ST) { s = 0; ph ^= 1; }
           }
       }
-    } else if (warp == 1 && rank == 0) {
+    } else if ((warp == 1 || warp == 3) && rank == 0) {
       // ---------------------------------------------------------- MMA
-      if (lane == 0) {
+      if (elect_one()) {
+        const int h = warp == 1 ? 0 : 1;
         int s = 0, pb = 0;
         uint32_t ph = 0, pph = 0;
         bool ok = true, issued = false;
         for (int t = t0; ok && t < tiles; t += step) {
           for (int b = 0; b < p.kb; ++b) {
-            if (!mbar_wait_cluster(&acc_empty[pb], pph ^ 1, ctl()) || !mbar_wait(&full[s], ph, ctl()) ||
-                !mbar_wait_cluster(&peer_full[s], ph, ctl())) { ok = false; break; }
+            // (one after the other the three looks cost three latencies)
+            if (!mbar_try_wait3(&full[s], ph, &peer_full[s], ph, &acc_empty[h * 2 + pb], pph ^ 1) &&
+                (!block_wait(&full[s], ph, ctl()) || !block_wait(&peer_full[s], ph, ctl()) ||
+                 !block_wait(&acc_empty[h * 2 + pb], pph ^ 1, ctl()))) { ok = false; break; }
             tc_fence_after();
-            const uint32_t ab = smem_u32(smem + s * C::STAGE), bb = ab + C::A_BYTES;
+            const uint32_t ab = smem_u32(smem + s * C::STAGE), bb = ab + C::A_BYTES + h * 8192;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f8_pair(tmem + pb * 256, sdesc_sw128(ab + kk * 32), sdesc_sw128(bb + kk * 32), C::IDESC, kk > 0 ? 1u : 0u);
+              mma_f8_pair(tmem + pb * 256 + h * 128, sdesc_sw128(ab + kk * 32), sdesc_sw128(bb + kk * 32), C::IDESC, kk > 0 ? 1u : 0u);
             issued = true;
             tc_commit_pair(&empty[s]);
-            tc_commit_pair(&acc_full[pb]);
+            tc_commit_pair(&acc_full[h * 2 + pb]);
             if (++s == C::ST) { s = 0; ph ^= 1; }
             if (++pb == C::PB) { pb = 0; pph ^= 1; }
           }
         }
         if (issued) {
-          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain + h))
                        : "memory");
-          mbar_wait(drain, 0, ctl_drain());
+          block_wait(drain + h, 0, ctl_drain());
         }
       }
     }
@@ -639,7 +711,7 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
     // ------------------------------------------------------------ scaling, sum and output
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_HIGH));
     if constexpr (!GROUPED) pdl_wait();
-    const int qd = warp & 3, h = (warp - 4) >> 2;
+    const int qd = warp & 3, h = (warp - 4) >> 2;   // 32 rows x half h of the tile's columns
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
     const uint32_t empty_addr = dsmem_addr(acc_empty, 0);
     int pb = 0;
@@ -666,48 +738,67 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (bg + i >= p.kb) break;
-          if (!mbar_wait_warp(&acc_full[pb], pph, ctl())) { ok = false; break; }
+          if (!block_wait_warp(&acc_full[h * 2 + pb], pph, ctl())) { ok = false; break; }
           tc_fence_after();
           const uint32_t ta = tmem + lane_base + pb * 256 + h * 128;
 #pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            float v[32];
-            tmem_ld_n<32>(ta + c0, v);
-            tmem_wait_regs<32>(v);
+          for (int c0 = 0; c0 < 128; c0 += 16) {
+            float v[16];
+            tmem_ld_n<16>(ta + c0, v);
+            tmem_wait_regs<16>(v);
+            if (c0 + 16 == 128) {   // the buffer is free as soon as the last columns have arrived
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(empty_addr + (h * 2 + pb) * 8);
+            }
 #pragma unroll
-            for (int c = 0; c < 32; ++c) acc[c0 + c] = fmaf(v[c], sc[i], acc[c0 + c]);
+            for (int c = 0; c < 16; ++c) acc[c0 + c] = fmaf(v[c], sc[i], acc[c0 + c]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(empty_addr + pb * 8);
           if (++pb == C::PB) { pb = 0; pph ^= 1; }
         }
       }
       if (!ok) break;
-      if (live && live_n) {
-        __nv_bfloat16* y = p.y + (size_t)m * p.N + n0;
+      // out through shared memory, 32 columns at a time, so that a store
+      // instruction covers 64-byte pieces of 8 rows (straight from
+      // the registers each one would touch 32 rows)
+      if (live_n) {
         const __nv_bfloat16* bias = p.bias ? p.bias + (size_t)tl.e * p.N + n0 : nullptr;
-        const int nn = p.N - n0;
-        if (p.vec_y && nn >= 128) {
+        const int nn = p.N - n0, mw = tl.m0 + rank * 128 + qd * 32, rows = min(32, tl.m_end - mw);
+        uint8_t* stage = smem + C::OUT_OFF + (warp - 4) * 32 * C::OUT_PITCH;
+        uint8_t* mine = stage + lane * C::OUT_PITCH;
 #pragma unroll
-          for (int c = 0; c < 128; c += 8) {
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              float a = acc[c + 2 * k], b = acc[c + 2 * k + 1];
+              float a = acc[c0 + c + 2 * k], b = acc[c0 + c + 2 * k + 1];
               if (bias) {
-                a += __bfloat162float(bias[c + 2 * k]);
-                b += __bfloat162float(bias[c + 2 * k + 1]);
+                const int at = c0 + c + 2 * k;
+                a += at < nn ? __bfloat162float(bias[at]) : 0.f;
+                b += at + 1 < nn ? __bfloat162float(bias[at + 1]) : 0.f;
               }
               const __nv_bfloat162 v2 = __floats2bfloat162_rn(a, b);
               w[k] = *reinterpret_cast<const uint32_t*>(&v2);
             }
-            *reinterpret_cast<uint4*>(y + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            sts128(mine + c * 2, make_uint4(w[0], w[1], w[2], w[3]));
           }
-        } else {
+          __syncwarp();
+          __nv_bfloat16* y = p.y + (size_t)mw * p.N + n0 + c0;
+          if (p.vec_y) {
+            const int c = (lane & 3) * 8;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c < nn) y[c] = __float2bfloat16_rn(acc[c] + (bias ? __bfloat162float(bias[c]) : 0.f));
+            for (int r = lane >> 2; r < 32; r += 8) {
+              const uint4 v = lds128(stage + r * C::OUT_PITCH + c * 2);
+              if (r < rows && c0 + c < nn) *reinterpret_cast<uint4*>(y + (size_t)r * p.N + c) = v;
+            }
+          } else {
+            if (c0 + lane < nn)
+              for (int r = 0; r < rows; ++r)
+                y[(size_t)r * p.N + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + r * C::OUT_PITCH + lane * 2);
+          }
+          __syncwarp();
         }
       }
     }

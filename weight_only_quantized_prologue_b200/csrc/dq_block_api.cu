@@ -203,7 +203,8 @@ dqgemm_status run_codes(dqgemm_handle h, const void* q, const float* sx, int M, 
   p.timeout_ns = h->timeout_ns;
   p.drain_ns = std::max(timeout_ns(), kDefaultTimeoutNs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_err(offsets ? launch_plan<true>(pl, h->wmap, tx, p, s) : launch_plan<false>(pl, h->wmap, tx, p, s));
+  const CUtensorMap& tw = pl.pair ? h->wmap64 : h->wmap;
+  return cuda_err(offsets ? launch_plan<true>(pl, tw, tx, p, s) : launch_plan<false>(pl, tw, tx, p, s));
 }
 
 }  // namespace
@@ -253,7 +254,8 @@ dqgemm_status block_create(dqgemm_handle* out, int E, int K, int N, const void* 
   }
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = set_attrs();
-  if (e != cudaSuccess || !make_q_map(&h->wmap, h->wchunks, (int)rows, K, 128)) {
+  if (e != cudaSuccess || !make_q_map(&h->wmap, h->wchunks, (int)rows, K, 128) ||
+      !make_q_map(&h->wmap64, h->wchunks, (int)rows, K, 64)) {
     dqgemm_destroy(h);
     return DQ_ERR_CUDA;
   }

@@ -46,7 +46,7 @@ struct dqgemm_s {
   // block-scaled FP8 (fmt == FMT_FP8B): wchunks holds the canonical codes
   // [E * N, K], col_scale the block scales [E][N / 128][K / 128] (rounded up)
   int E = 1;
-  CUtensorMap wmap;                 // boxes of 128 k x 128 rows of the codes
+  CUtensorMap wmap, wmap64;         // boxes of 128 k x 128 (64) rows of the codes
   std::mutex maps_mu;               // run entry points may be called from several threads
 };
 
