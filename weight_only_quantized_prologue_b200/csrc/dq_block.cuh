@@ -173,12 +173,14 @@ __device__ __forceinline__ bool mbar_try_wait3(uint64_t* a, uint32_t pa, uint64_
 }
 // the whole warp: every lane observes the phase itself
 __device__ __forceinline__ bool block_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtl ctl) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = block_wait(bar, parity, ctl) ? 1 : 0;
-  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-  if (ok) mbar_try_wait(bar, parity);
-  return ok != 0;
+  uint64_t t0 = 0;
+  for (int i = ctl.timeout_ns < 1000u ? 63 : 0;; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 63) == 63) {
+      if (t0 == 0) t0 = globaltimer_ns();
+      if (__any_sync(0xFFFFFFFFu, wait_give_up(ctl, t0))) return false;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -558,19 +560,30 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// shared -> global, complete in the issuing thread's bulk group
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile(
+      "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(dst),
+      "r"(smem_u32(src)), "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 struct PairCfg {
   static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int ST = 5;
+  static constexpr int ST = 4;
   static constexpr int PB = 2;                  // partial buffers of 2 x 128 columns: all of TMEM
   static constexpr int TMEM_COLS = 512;
   static constexpr int BAR_OFF = ST * STAGE;
   static constexpr int BAR_BYTES = 256;
-  // output staging: per epilogue warp 32 rows of 32 bf16, rows 80 bytes apart
-  // (16-byte pieces of 8 neighbouring rows then lie in different banks)
-  static constexpr int OUT_PITCH = 80;
+  // output staging: a row of 128 bf16 per epilogue thread, rows 272 bytes
+  // apart (16-byte pieces of 8 neighbouring rows then lie in different banks)
+  static constexpr int OUT_PITCH = 272;
   static constexpr int OUT_OFF = BAR_OFF + BAR_BYTES;
-  static constexpr int OUT_BYTES = 8 * 32 * OUT_PITCH;
+  static constexpr int OUT_BYTES = 256 * OUT_PITCH;
   static constexpr int TAB_OFF = OUT_OFF + OUT_BYTES;
   static constexpr int SMEM = TAB_OFF + (MAX_EXPERTS + 1) * 4 + 1024;
   static constexpr int THREADS = 384;   // 4 warps of copies and MMAs, 8 of sums
@@ -758,50 +771,44 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
         }
       }
       if (!ok) break;
-      // out through shared memory, 32 columns at a time, so that a store
-      // instruction covers 64-byte pieces of 8 rows (straight from
-      // the registers each one would touch 32 rows)
+      // Out through shared memory: each thread leaves its row there and hands
+      // it to the copy engine, which writes it while the next tile is summed
+      // (stores from the registers touch 32 rows an instruction: 5000 cycles
+      // a tile against 32 x 512 of MMAs).
       if (live_n) {
         const __nv_bfloat16* bias = p.bias ? p.bias + (size_t)tl.e * p.N + n0 : nullptr;
-        const int nn = p.N - n0, mw = tl.m0 + rank * 128 + qd * 32, rows = min(32, tl.m_end - mw);
-        uint8_t* stage = smem + C::OUT_OFF + (warp - 4) * 32 * C::OUT_PITCH;
-        uint8_t* mine = stage + lane * C::OUT_PITCH;
+        const int nn = min(128, p.N - n0);
+        uint8_t* mine = smem + C::OUT_OFF + (threadIdx.x - 128) * C::OUT_PITCH;
+        bulk_wait_read();   // this thread's last row has left
+        if (bias) {
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
+          for (int c = 0; c < 128; ++c) acc[c] += c < nn ? __bfloat162float(bias[c]) : 0.f;
+        }
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            uint32_t w[4];
+        for (int c = 0; c < 128; c += 8) {
+          uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float a = acc[c0 + c + 2 * k], b = acc[c0 + c + 2 * k + 1];
-              if (bias) {
-                const int at = c0 + c + 2 * k;
-                a += at < nn ? __bfloat162float(bias[at]) : 0.f;
-                b += at + 1 < nn ? __bfloat162float(bias[at + 1]) : 0.f;
-              }
-              const __nv_bfloat162 v2 = __floats2bfloat162_rn(a, b);
-              w[k] = *reinterpret_cast<const uint32_t*>(&v2);
-            }
-            sts128(mine + c * 2, make_uint4(w[0], w[1], w[2], w[3]));
+          for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 v2 = __floats2bfloat162_rn(acc[c + 2 * k], acc[c + 2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&v2);
           }
+          sts128(mine + c * 2, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+        if (p.vec_y) {   // (N a multiple of 8: whole 16-byte pieces)
+          fence_proxy_async_smem();
+          if (live) bulk_s2g(p.y + (size_t)m * p.N + n0, mine, (uint32_t)nn * 2);
+        } else {
           __syncwarp();
-          __nv_bfloat16* y = p.y + (size_t)mw * p.N + n0 + c0;
-          if (p.vec_y) {
-            const int c = (lane & 3) * 8;
-#pragma unroll
-            for (int r = lane >> 2; r < 32; r += 8) {
-              const uint4 v = lds128(stage + r * C::OUT_PITCH + c * 2);
-              if (r < rows && c0 + c < nn) *reinterpret_cast<uint4*>(y + (size_t)r * p.N + c) = v;
-            }
-          } else {
-            if (c0 + lane < nn)
-              for (int r = 0; r < rows; ++r)
-                y[(size_t)r * p.N + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + r * C::OUT_PITCH + lane * 2);
-          }
+          const int mw = m - lane, rows = min(32, tl.m_end - mw);
+          for (int r = 0; r < rows; ++r)
+            for (int c = lane; c < nn; c += 32)
+              p.y[(size_t)(mw + r) * p.N + n0 + c] =
+                  *reinterpret_cast<const __nv_bfloat16*>(mine + (r - lane) * C::OUT_PITCH + c * 2);
           __syncwarp();
         }
       }
     }
+    bulk_wait_all();
     if (!ok) *abort_flag = 1;
     __syncwarp();
   }
