@@ -219,8 +219,8 @@ dqgemm_status dqgemm_run_static_mlp(dqgemm_handle l1, dqgemm_handle l2, const vo
  * q u8 [M, K] with scales fp32 [M, ceil(K/128)] as dqgemm_quantize_act_fp8_block,
  * dqgemm_rmsnorm and dqgemm_silu_mul write them.  y: device bf16 [M, N].  One
  * launch, no workspace: calls on one handle may run on several streams at
- * once.  (dqgemm_run on such a handle quantizes x into a workspace of the
- * handle first and is bound by what it says about W4A4 handles: first call of
+ * once.  (dqgemm_run on such a handle is dqgemm_run_fp8_block with a workspace
+ * of the handle, and bound by what it says about W4A4 handles: first call of
  * the largest M before any capture, calls stream-ordered.)
  * DQ_ERR_UNSUPPORTED for other formats and for experts. */
 dqgemm_status dqgemm_run_fp8_block_quantized(dqgemm_handle h, const void* q, const float* scales, int M, void* y,
@@ -243,6 +243,19 @@ dqgemm_status dqgemm_create_experts(dqgemm_handle* out, dqgemm_format fmt, int E
  * whose end lies before its start has no rows.  One launch, no workspace. */
 dqgemm_status dqgemm_run_experts_quantized(dqgemm_handle h, const void* q, const float* scales, int M, const int* offsets,
                                            void* y, void* stream);
+
+/* A block-scaled layer (offsets NULL) or experts on bf16 x [M, K], with the
+ * workspace in the caller's hands.  Few rows (M <= 8; with offsets M <= 16 or
+ * M <= 4 E) are quantized in the product's own kernel and need none: one
+ * launch.  Else x is quantized into `workspace` first: two launches, chained.
+ * workspace: device, 16-byte aligned, at least dqgemm_plan.workspace_bytes of
+ * dqgemm_get_plan(h, M) (an upper bound for every call of up to M rows is
+ * M * (K + 4 * ceil(K/128)) + 256); DQ_ERR_INVALID_ARG if it is missing or
+ * smaller.  Nobody else may use it before the call's kernels are done.  The
+ * result is the same as from dqgemm_quantize_act_fp8_block and the call on
+ * its codes, bit by bit. */
+dqgemm_status dqgemm_run_fp8_block(dqgemm_handle h, const void* x, int M, const int* offsets, void* y, void* workspace,
+                                   long long workspace_bytes, void* stream);
 
 /* Release the handle and its device memory.  Synchronizes the device (the
  * CUDA runtime's cudaFree does so in any case); no kernel of the handle may

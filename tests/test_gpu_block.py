@@ -116,6 +116,46 @@ def test_linear_on_bf16_is_the_quantizer_and_the_product(M):
         assert torch.equal(y1, y2)
 
 
+@pytest.mark.parametrize("M,K,N", [(1, 16, 1), (1, 8192, 128), (1, 2064, 14336), (3, 144, 130), (8, 4096, 512), (7, 400, 300),
+                                   (8, 2064, 1000), (5, 128, 128), (9, 1040, 100), (32, 2064, 1000)])
+def test_few_rows_quantized_in_the_products_kernel_give_the_same_bits(M, K, N):
+    x, _, _ = rows(M, K, 25)
+    wq, ws = weights(1, N, K, 27)
+    b = randn((N,), 28).to(torch.bfloat16).cuda()
+    lin = dq.QuantizedLinear("fp8_block", K, N, cuda(wq[0]), cuda(ws[0]), bias=b)
+    assert (lin.plan(M)["workspace_bytes"] == 0) == (M <= 8)
+    x[0, ::3] = 0
+    x = x.cuda()
+    q, s = dq.quantize_act_fp8_block(x)
+    out = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = lin(x, out=out[:M])
+    assert torch.equal(y, lin.from_codes(q, scales=s)) and (out[M:] == 7).all() and lin.last_error() == 0
+
+
+@pytest.mark.parametrize("counts", [[0, 3, 0, 1], [1] * 16, [16, 0], [9, 0, 7, 0, 17, 0, 0, 0, 0, 3, 1, 0], [40, 0, 0, 2, 1, 0, 7],
+                                    [0, 0, 33]], ids=str)
+@pytest.mark.parametrize("K,N", [(400, 300), (1024, 128)])
+def test_experts_on_bf16_give_the_bits_of_their_codes(counts, K, N):
+    E, M = len(counts), sum(counts)
+    x, _, _ = rows(M, K, 33)
+    wq, ws = weights(E, N, K, 35)
+    ex = dq.QuantizedExperts("fp8_block", E, K, N, cuda(wq), cuda(ws))
+    off = cuda(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    x = x.cuda()
+    q, s = dq.quantize_act_fp8_block(x)
+    ref = ex.from_codes(q, s, off)
+    assert torch.equal(ex(x, off), ref) and ex.last_error() == 0
+    ws = torch.empty(M * (K + 4 * ((K + 127) // 128)) + 256, dtype=torch.uint8, device="cuda")
+    y = torch.empty_like(ref)
+    dq.dqgemm_run_fp8_block(ex.handle, x, M, off, y, ws, ws.numel())
+    assert torch.equal(y, ref)
+    need = ex.plan(M)["workspace_bytes"]
+    assert need <= ws.numel() and (need > 0 or M <= max(16, 4 * E))
+    if need:
+        with pytest.raises(dq.DQError):
+            dq.dqgemm_run_fp8_block(ex.handle, x, M, off, y, ws, need - 1)
+
+
 def test_packers_and_dequantize_are_bit_exact():
     N, K = 200, 336
     w = (randn((N, K), 31) * 0.1).float()

@@ -29,6 +29,7 @@ from ._native import (  # noqa: F401
     dqgemm_rmsnorm,
     dqgemm_run,
     dqgemm_run_experts_quantized,
+    dqgemm_run_fp8_block,
     dqgemm_run_fp8_block_quantized,
     dqgemm_run_fp8_static_quantized,
     dqgemm_run_fp8_static_quantized_out,
@@ -115,29 +116,24 @@ def static_mlp(l1, l2, x, out=None, h_out=None, stream=None):
 
 
 def _block_call(layer, x, M, offsets, out, stream):
-    """A block-scaled layer (or experts, with their offsets) on bf16 x:
-    quantize, then the product.  The codes and scales between the two live in
-    one temporary of the stream the calls run on, so that the allocator hands
-    it to nobody before they are done."""
-    torch = _torch()
-    L, dev, K = _native.lib(), layer._dev, layer.K
+    """A block-scaled layer (or experts, with their offsets) on bf16 x.  With
+    more than the few rows that the product's own kernel quantizes, their
+    codes and scales go through a temporary of the stream the call runs on, so
+    that the allocator hands it to nobody before the call is done."""
+    dev = layer._dev
     s = _native.device_stream(stream, dev)
-    nq = (M * K + 255) // 256 * 256
-    size = nq + 4 * M * ((K + 127) // 128)
-    if stream is None:
-        tmp = torch.empty(size, dtype=torch.uint8, device=layer.device)
-    else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(s, device=layer.device)):
-            tmp = torch.empty(size, dtype=torch.uint8, device=layer.device)
-    q = tmp.data_ptr()
-    _native._check(L.dqgemm_quantize_act_fp8_block(0, x.data_ptr(), K, M, K, q, q + nq, s),
-                   "dqgemm_quantize_act_fp8_block")
-    if offsets is None:
-        _native._check(L.dqgemm_run_fp8_block_quantized(layer._h, q, q + nq, M, out.data_ptr(), s),
-                       "dqgemm_run_fp8_block_quantized")
-    else:
-        _native._check(L.dqgemm_run_experts_quantized(layer._h, q, q + nq, M, offsets.data_ptr(), out.data_ptr(), s),
-                       "dqgemm_run_experts_quantized")
+    size = ws = 0
+    if M > layer._few_rows:
+        torch = _torch()
+        size = M * (layer.K + 4 * ((layer.K + 127) // 128)) + 256
+        if stream is None:
+            tmp = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=layer.device)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=layer.device)):
+                tmp = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=layer.device)
+        ws = tmp.data_ptr()
+    _native._check(_native.lib().dqgemm_run_fp8_block(layer._h, x.data_ptr(), M, offsets, out.data_ptr(), ws or None, size, s),
+                   "dqgemm_run_fp8_block")
 
 
 class QuantizedLinear:
@@ -147,6 +143,9 @@ class QuantizedLinear:
     ``fmt`` (see ``storage_shapes``); they are copied and re-laid-out by the
     library, so the caller may drop them afterwards."""
 
+    # rows up to which the library quantizes a block-scaled layer's bf16 x in
+    # the product's kernel, so that a call needs no workspace
+    _few_rows = 8
     # static FP8 from this many rows on: quantize x once, then the FP8 GEMM
     # (the fused kernel re-quantizes x for every 128-channel tile) ...
     STATIC_PREQUANT_M = 128
@@ -212,7 +211,8 @@ class QuantizedLinear:
 
     def _out(self, out, M, dtype):
         if out is None:
-            return _torch().empty((M, self.N), dtype=dtype, device=self.device)
+            # (empty_strided: the cheapest of torch's allocating calls on the host)
+            return _torch().empty_strided((M, self.N), (self.N, 1), dtype=dtype, device=self.device)
         if not _fits(out, self.N, dtype, M, self._dev):
             _require(out, "out", shape=(M, self.N), dtype=dtype, device=self.device)
         return out
@@ -340,6 +340,7 @@ class QuantizedExperts:
         self.device = packed.device
         self._dev = self.device.index
         self._check_current = torch.cuda.device_count() > 1
+        self._few_rows = max(16, 4 * E)           # as QuantizedLinear's
         self._h = dqgemm_create_experts(fmt, E, K, N, packed, scales, bias)
 
     @classmethod
@@ -377,7 +378,7 @@ class QuantizedExperts:
         self._check_offsets(offsets)
         out = self._out(out, M, torch.bfloat16)
         if M:
-            _block_call(self, x, M, offsets, out, stream)
+            _block_call(self, x, M, offsets.data_ptr(), out, stream)
         return out
 
     def from_codes(self, q, scales, offsets, out=None, stream=None):

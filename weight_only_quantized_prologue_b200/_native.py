@@ -60,6 +60,7 @@ _SIGNATURES = {
     "dqgemm_run_static_mlp": [_VP, _VP, _VP, _I, _VP, _VP, _VP],
     "dqgemm_run_fp8_block_quantized": [_VP, _VP, _VP, _I, _VP, _VP],
     "dqgemm_create_experts": [ctypes.POINTER(_VP), _I, _I, _I, _I, _VP, _VP, _VP],
+    "dqgemm_run_fp8_block": [_VP, _VP, _I, _VP, _VP, _VP, _LL, _VP],
     "dqgemm_run_experts_quantized": [_VP, _VP, _VP, _I, _VP, _VP, _VP],
     "dqgemm_rmsnorm": [_I, _VP, _LL, _VP, _VP, _I, _VP, _F, _I, _I, _I, _F, _VP, _VP, _VP],
     "dqgemm_silu_mul": [_I, _VP, _LL, _I, _I, _I, _F, _VP, _VP, _VP],
@@ -213,6 +214,11 @@ def dqgemm_create_experts(fmt, E, K, N, packed_w, scales, bias=None):
     _check(lib().dqgemm_create_experts(ctypes.byref(h), FORMATS[fmt], E, K, N, _ptr(packed_w), _ptr(scales), _ptr(bias)),
            "dqgemm_create_experts")
     return h
+
+
+def dqgemm_run_fp8_block(h, x, M, offsets, y, workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().dqgemm_run_fp8_block(h, _ptr(x), int(M), _ptr(offsets), _ptr(y), _ptr(workspace), workspace_bytes,
+                                      _stream(stream)), "dqgemm_run_fp8_block")
 
 
 def dqgemm_run_experts_quantized(h, q, scales, M, offsets, y, stream=None):

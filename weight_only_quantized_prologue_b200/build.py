@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libdqgemm.so")
 _COMMON = ["dq_handle.h", "dq_common.cuh", "dq_layout.h"]
 SOURCES = {
     "dq_api.cu": _COMMON + ["dq_gemm.cuh", "dq_aux.cuh", "dq_codec.h"],
-    "dq_block_api.cu": _COMMON + ["dq_block.cuh", "dq_codec.h"],
+    "dq_block_api.cu": _COMMON + ["dq_block.cuh", "dq_rows.cuh", "dq_codec.h"],
     "dq_rows_api.cu": _COMMON + ["dq_rows.cuh"],
 }
 OBJ = os.path.join(HERE, "_build")

@@ -29,6 +29,7 @@
 
 #include "dq_codec.h"
 #include "dq_common.cuh"
+#include "dq_rows.cuh"
 
 namespace dq {
 
@@ -36,12 +37,13 @@ constexpr int MAX_EXPERTS = 1024;
 
 struct BlockParams {
   const float* sx;             // [M, kb]
+  const __nv_bfloat16* x;      // activations that the kernel quantizes itself [M, K]
   const float* sw;             // [E][nb][kb]
   const __nv_bfloat16* bias;   // [E][N] or null
   __nv_bfloat16* y;            // [M, N]
   const int* offsets;          // grouped: device [E + 1]
   int* status;
-  int M, N, E;
+  int M, N, K, E;
   int kb, nb;                  // blocks along K and N
   int n_tiles, m_tiles;        // (m_tiles: dense)
   int split;
@@ -248,9 +250,17 @@ __device__ __forceinline__ void load_scales(const float* row, bool live, int b, 
 
 // ---------------------------------------------------------------------------
 // skinny: 128 channels x BN rows per CTA
-// warps: 0 weight copies, 1 MMA, 2 activation copies, 4..11 epilogue
+// warps: 0 weight copies, 1 MMA, 2 activation copies, 3 scales, 4..11
+// epilogue; with bf16 activations (XBF) 12..15 quantize them instead of 2 and 3
+//
+// The combined scales sx * sw of each block of K go through a ring of their
+// own, [SR][BN].  It needs no barrier against reuse: who writes entry i + SR
+// has seen the MMAs of block i + SR - ST done, hence those of block i + PB,
+// which were issued after the epilogue had finished with block i.  The MMAs
+// of a block wait for its scales too (through full_x): nobody falls a whole
+// phase of a barrier behind, where a parity would be taken for the next.
 // ---------------------------------------------------------------------------
-template <int BN>
+template <int BN, bool XBF>
 struct SkinnyCfg {
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_BYTES = BN * 128;
@@ -259,28 +269,92 @@ struct SkinnyCfg {
   // one at 128
   static constexpr int ST = BN == 16 ? 5 : BN == 32 ? 5 : BN == 64 ? 4 : 6;
   static constexpr int PB = 4;                             // partial buffers
+  static constexpr int SR = ST + PB;                       // scale entries
   static constexpr int TMEM_COLS = PB * BN < 32 ? 32 : PB * BN;
   static constexpr int HALF = BN / 2;                      // columns per epilogue thread
   static constexpr int BAR_OFF = ST * STAGE;
-  static constexpr int BAR_BYTES = 256;
-  static constexpr int SC_OFF = BAR_OFF + BAR_BYTES;       // [8 warps][2][HALF] combined scales
-  static constexpr int SC_BYTES = 8 * 2 * HALF * 4;
+  static constexpr int BAR_BYTES = 384;
+  static constexpr int SC_OFF = BAR_OFF + BAR_BYTES;
+  static constexpr int SC_BYTES = SR * BN * 4;
   static constexpr int TAB_OFF = SC_OFF + SC_BYTES;        // grouped: tile counts
   static constexpr int TAB_BYTES = (MAX_EXPERTS + 1) * 4;
   static constexpr int SMEM = TAB_OFF + TAB_BYTES + 1024;
   static constexpr int CTAS = BN <= 64 ? 2 : 1;
-  static constexpr int THREADS = 384;
+  static constexpr int THREADS = XBF ? 512 : 384;
   static_assert(X_BYTES % 1024 == 0, "swizzle atoms");
+  static_assert(!XBF || BN == 16, "the quantizing warps keep up with a few rows only");
   static_assert(BN * 128 * 4 <= ST * STAGE, "the reduction reuses the ring");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
   static_assert(CTAS * TMEM_COLS <= 512, "tensor memory");
 };
 
-template <int BN, bool GROUPED>
-__global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
+// One block of K of a tile's rows: 16 lanes a row, 8 elements a lane, two rows
+// an instruction.  Codes into the tensor core's swizzled rows, combined scales
+// into `sc`.  The same arithmetic as the row quantizer's.  Rows past m_end are
+// left out: what their columns hold is not stored.
+__device__ __forceinline__ void quantize_stage(const __nv_bfloat16* x, int K, int m0, int rows, int b, float sw, uint8_t* xs,
+                                               float* sc, int lane) {
+  const int k = b * 128 + (lane & 15) * 8, half = lane >> 4;
+  const __nv_bfloat16* src = x + (size_t)(m0 + half) * K + k;
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    // four row pairs at once: loads, maxima and quotients of one overlap the others'
+    uint4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u[i] = r0 + 2 * i + half < rows && k < K ? *reinterpret_cast<const uint4*>(src + (size_t)(r0 + 2 * i) * K)
+                                               : make_uint4(0u, 0u, 0u, 0u);
+    // the maxima as bf16 bits, two pairs of rows in a word
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu),
+                                  __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu));
+      m[i] = max(w & 0xFFFFu, w >> 16);
+    }
+    uint32_t m01 = m[0] | (m[1] << 16), m23 = m[2] | (m[3] << 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
+      m01 = __vmaxu2(m01, __shfl_xor_sync(0xFFFFFFFFu, m01, o));
+      m23 = __vmaxu2(m23, __shfl_xor_sync(0xFFFFFFFFu, m23, o));
+    }
+    m[0] = m01 << 16;
+    m[1] = m01 & 0xFFFF0000u;
+    m[2] = m23 << 16;
+    m[3] = m23 & 0xFFFF0000u;
+    BlockScale bs[4];
+    bool fast = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      bs[i] = block_scale_of(m[i]);
+      fast = fast && bs[i].fast;
+    }
+    fast = __all_sync(0xFFFFFFFFu, fast);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 2 * i + half;   // (below the tile's 16: the rows that fill the last eight hold zeros)
+      float v[8];
+      unpack2(u[i].x, v[0], v[1], __nv_bfloat16());
+      unpack2(u[i].y, v[2], v[3], __nv_bfloat16());
+      unpack2(u[i].z, v[4], v[5], __nv_bfloat16());
+      unpack2(u[i].w, v[6], v[7], __nv_bfloat16());
+      uint2 c;
+      if (fast) {
+        c = codes8_fast(v, bs[i].s, bs[i].r);
+      } else {
+        bs[i].s = __fdiv_rn(__uint_as_float(m[i]), 448.f);
+        c = codes8_any(v, bs[i].s);
+      }
+      if ((lane & 15) == 0) sc[r] = bs[i].s * sw;
+      *reinterpret_cast<uint2*>(xs + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8) = c;
+    }
+  }
+}
+
+template <int BN, bool GROUPED, bool XBF>
+__global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, SkinnyCfg<BN, XBF>::CTAS)
     block_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                         const BlockParams p) {
-  using C = SkinnyCfg<BN>;
+  using C = SkinnyCfg<BN, XBF>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full_w = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
@@ -288,11 +362,13 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
   uint64_t* empty = full_x + C::ST;          // stage read by the MMAs
   uint64_t* acc_full = empty + C::ST;        // [PB]
   uint64_t* acc_empty = acc_full + C::PB;    // [PB]
-  uint64_t* drain = acc_empty + C::PB;
+  uint64_t* sc_full = acc_empty + C::PB;     // [SR] scales written
+  uint64_t* drain = sc_full + C::SR;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);   // an epilogue warp gave up
-  static_assert((3 * C::ST + 2 * C::PB + 1) * 8 + 12 <= C::BAR_BYTES, "barriers");
+  static_assert((3 * C::ST + 2 * C::PB + C::SR + 1) * 8 + 12 <= C::BAR_BYTES, "barriers");
+  float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
   int* start = reinterpret_cast<int*>(smem + C::TAB_OFF);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -302,13 +378,14 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(&full_w[s], 1);
-      mbar_init(&full_x[s], 1);
+      mbar_init(&full_x[s], XBF ? 1 : 2);   // a quantizing warp, or copies and scales
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < C::PB; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 8);
     }
+    for (int b = 0; b < C::SR; ++b) mbar_init(&sc_full[b], 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *bad = 0;
@@ -354,7 +431,7 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
       for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) block_wait(&full_w[i % C::ST], (i / C::ST) & 1, ctl_drain());
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (!XBF && warp == 2) {
     // ------------------------------------------------------------ activation copies
     if (elect_one()) {
       if constexpr (!GROUPED) pdl_wait();
@@ -373,6 +450,77 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
       for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) block_wait(&full_x[i % C::ST], (i / C::ST) & 1, ctl_drain());
     }
     __syncwarp();
+  } else if (!XBF && warp == 3) {
+    // ------------------------------------------------------------ scales, fetched four blocks ahead
+    if constexpr (!GROUPED) pdl_wait();
+    constexpr int CPL = (BN + 31) / 32;                 // rows per lane
+    int it = 0, s = 0, e = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int t = t0; ok && t < tiles; t += step) {
+      const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
+      const float* sw = p.sw + ((size_t)tl.e * p.nb + (tl.n0 >> 7)) * p.kb;
+      const float* sx[CPL];
+      bool live[CPL];
+      float nx[CPL][4], nw[4];
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) {
+        const int m = tl.m0 + lane + 32 * j;
+        live[j] = lane + 32 * j < BN && m < tl.m_end;
+        sx[j] = p.sx + (size_t)(live[j] ? m : 0) * p.kb;
+        load_scales(sx[j], live[j], b0, b1, nx[j]);
+      }
+      load_scales(sw, true, b0, b1, nw);
+      for (int bg = b0; ok && bg < b1; bg += 4) {
+        float c[CPL][4];
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[j][i] = nx[j][i] * nw[i];
+          load_scales(sx[j], live[j], bg + 4, b1, nx[j]);
+        }
+        load_scales(sw, true, bg + 4, b1, nw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (bg + i >= b1) break;
+          if (it >= C::ST && !block_wait_warp(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
+#pragma unroll
+          for (int j = 0; j < CPL; ++j)
+            if (lane + 32 * j < BN) scales[e * BN + lane + 32 * j] = c[j][i];
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full_x[s]);
+            mbar_arrive(&sc_full[e]);
+          }
+          ++it;
+          if (++s == C::ST) { s = 0; ph ^= 1; }
+          if (++e == C::SR) e = 0;
+        }
+      }
+    }
+  } else if (XBF && warp >= 12) {
+    // ------------------------------------------------------------ quantizer: warp w takes every fourth block
+    if constexpr (!GROUPED) pdl_wait();
+    const int w = warp - 12;
+    int it = 0;
+    bool ok = true;
+    for (int t = t0; ok && t < tiles; t += step) {
+      const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
+      const float* sw = p.sw + ((size_t)tl.e * p.nb + (tl.n0 >> 7)) * p.kb;
+      const int rows = min(BN, tl.m_end - tl.m0);
+      for (int b = b0; b < b1; ++b, ++it) {
+        if ((it & 3) != w) continue;
+        const int s = it % C::ST, e = it % C::SR;
+        if (it >= C::ST && !block_wait_warp(&empty[s], (uint32_t)(it / C::ST + 1) & 1u, ctl())) { ok = false; break; }
+        quantize_stage(p.x, p.K, tl.m0, rows, b, sw[b], smem + s * C::STAGE + C::W_BYTES, scales + e * BN, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full_x[s]);
+          mbar_arrive(&sc_full[e]);
+        }
+      }
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (elect_one()) {
@@ -381,8 +529,9 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
       bool ok = true, issued = false;
       for (int t = t0; ok && t < tiles; t += step) {
         for (int b = b0; b < b1; ++b) {
-          if (!block_wait(&acc_empty[pb], pph ^ 1, ctl()) || !block_wait(&full_w[s], ph, ctl()) ||
-              !block_wait(&full_x[s], ph, ctl())) { ok = false; break; }
+          if (!mbar_try_wait3(&full_w[s], ph, &full_x[s], ph, &acc_empty[pb], pph ^ 1) &&
+              (!block_wait(&full_w[s], ph, ctl()) || !block_wait(&full_x[s], ph, ctl()) ||
+               !block_wait(&acc_empty[pb], pph ^ 1, ctl()))) { ok = false; break; }
           tc_fence_after();
           const uint32_t wb = smem_u32(smem + s * C::STAGE), xb = wb + C::W_BYTES;
 #pragma unroll
@@ -401,76 +550,44 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ scaling, sum and output
     if constexpr (!GROUPED) pdl_wait();
     const int qd = warp & 3, h = (warp - 4) >> 2;
     const int r = qd * 32 + lane;                       // channel within the tile
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
-    float* sc = reinterpret_cast<float*>(smem + C::SC_OFF) + (warp - 4) * 2 * C::HALF;
-    constexpr int CPL = (C::HALF + 31) / 32;            // columns whose scales this lane fetches
     constexpr int LD = C::HALF < 16 ? C::HALF : 16;
-    int pb = 0;
-    uint32_t pph = 0;
+    int pb = 0, e = 0;
+    uint32_t pph = 0, eph = 0;
     bool ok = true;
     for (int t = t0; ok && t < tiles; t += step) {
       const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
-      const float* sw = p.sw + ((size_t)tl.e * p.nb + (tl.n0 >> 7)) * p.kb;
-      const float* sxr[CPL];
-      bool live[CPL];
-#pragma unroll
-      for (int j = 0; j < CPL; ++j) {
-        const int c = lane + 32 * j, m = tl.m0 + h * C::HALF + c;
-        live[j] = c < C::HALF && m < tl.m_end;
-        sxr[j] = p.sx + (size_t)(live[j] ? m : 0) * p.kb;
-      }
-      float nx[CPL][4], nw[4], cx[CPL][4], cw[4];
-#pragma unroll
-      for (int j = 0; j < CPL; ++j) load_scales(sxr[j], live[j], b0, b1, nx[j]);
-      load_scales(sw, true, b0, b1, nw);
       float acc[C::HALF];
 #pragma unroll
       for (int i = 0; i < C::HALF; ++i) acc[i] = 0.f;
-      for (int bg = b0; ok && bg < b1; bg += 4) {
-        // this group's scales arrived while the last group was summed
+      for (int b = b0; b < b1; ++b) {
+        if (!block_wait_warp(&sc_full[e], eph, ctl()) || !block_wait_warp(&acc_full[pb], pph, ctl())) { ok = false; break; }
+        tc_fence_after();
+        const float* f = scales + e * BN + h * C::HALF;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cw[i] = nw[i];
+        for (int c0 = 0; c0 < C::HALF; c0 += LD) {
+          float v[LD];
+          tmem_ld_n<LD>(tmem + lane_base + pb * BN + h * C::HALF + c0, v);
+          tmem_wait_regs<LD>(v);
 #pragma unroll
-          for (int j = 0; j < CPL; ++j) cx[j][i] = nx[j][i];
-        }
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) load_scales(sxr[j], live[j], bg + 4, b1, nx[j]);
-        load_scales(sw, true, bg + 4, b1, nw);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (bg + i >= b1) break;
-          float* buf = sc + (i & 1) * C::HALF;
-#pragma unroll
-          for (int j = 0; j < CPL; ++j)
-            if (lane + 32 * j < C::HALF) buf[lane + 32 * j] = cx[j][i] * cw[i];
-          __syncwarp();
-          if (!block_wait_warp(&acc_full[pb], pph, ctl())) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
-          for (int c0 = 0; c0 < C::HALF; c0 += LD) {
-            float v[LD];
-            tmem_ld_n<LD>(tmem + lane_base + pb * BN + h * C::HALF + c0, v);
-            tmem_wait_regs<LD>(v);
-#pragma unroll
-            for (int c = 0; c < LD; c += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(buf + c0 + c);
-              acc[c0 + c] = fmaf(v[c], f.x, acc[c0 + c]);
-              acc[c0 + c + 1] = fmaf(v[c + 1], f.y, acc[c0 + c + 1]);
-              acc[c0 + c + 2] = fmaf(v[c + 2], f.z, acc[c0 + c + 2]);
-              acc[c0 + c + 3] = fmaf(v[c + 3], f.w, acc[c0 + c + 3]);
-            }
+          for (int c = 0; c < LD; c += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(f + c0 + c);
+            acc[c0 + c] = fmaf(v[c], q.x, acc[c0 + c]);
+            acc[c0 + c + 1] = fmaf(v[c + 1], q.y, acc[c0 + c + 1]);
+            acc[c0 + c + 2] = fmaf(v[c + 2], q.z, acc[c0 + c + 2]);
+            acc[c0 + c + 3] = fmaf(v[c + 3], q.w, acc[c0 + c + 3]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[pb]);
-          if (++pb == C::PB) { pb = 0; pph ^= 1; }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[pb]);
+        if (++pb == C::PB) { pb = 0; pph ^= 1; }
+        if (++e == C::SR) { e = 0; eph ^= 1; }
       }
       if (!ok) break;
       if (S == 1) {
@@ -500,7 +617,7 @@ __global__ void __launch_bounds__(384, SkinnyCfg<BN>::CTAS)
   if (S > 1) {
     __syncwarp();
     cluster_sync();   // every partial (or its absence) is in its CTA's shared memory
-    if (warp >= 4) {
+    if (warp >= 4 && warp < 12) {
       const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t0);
       const int cols = BN / S;                        // S is a power of two <= 8 <= BN
       bool good = true;

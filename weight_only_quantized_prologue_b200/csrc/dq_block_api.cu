@@ -27,18 +27,15 @@ struct BlockPlan {
   int grid;        // CTAs
 };
 
-template <int BN>
-struct Skinny {
-  using C = SkinnyCfg<BN>;
-  template <bool G>
-  static cudaError_t attr() {
-    cudaError_t e = cudaFuncSetAttribute(block_skinny_kernel<BN, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(block_skinny_kernel<BN, G>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               (int)cudaSharedmemCarveoutMaxShared);
-    return e;
-  }
-};
+template <int BN, bool G, bool X>
+cudaError_t skinny_attr() {
+  cudaError_t e = cudaFuncSetAttribute(block_skinny_kernel<BN, G, X>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       SkinnyCfg<BN, X>::SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(block_skinny_kernel<BN, G, X>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared);
+  return e;
+}
 
 template <bool G>
 cudaError_t pair_attr() {
@@ -51,9 +48,11 @@ cudaError_t pair_attr() {
 
 cudaError_t set_attrs() {
   cudaError_t e = cudaSuccess;
-  for (cudaError_t r : {Skinny<16>::attr<false>(), Skinny<32>::attr<false>(), Skinny<64>::attr<false>(),
-                        Skinny<128>::attr<false>(), Skinny<16>::attr<true>(), Skinny<32>::attr<true>(),
-                        Skinny<64>::attr<true>(), Skinny<128>::attr<true>(), pair_attr<false>(), pair_attr<true>()})
+  for (cudaError_t r :
+       {skinny_attr<16, false, false>(), skinny_attr<32, false, false>(), skinny_attr<64, false, false>(),
+        skinny_attr<128, false, false>(), skinny_attr<16, true, false>(), skinny_attr<32, true, false>(),
+        skinny_attr<64, true, false>(), skinny_attr<128, true, false>(), skinny_attr<16, false, true>(),
+        skinny_attr<16, true, true>(), pair_attr<false>(), pair_attr<true>()})
     if (e == cudaSuccess) e = r;
   return e;
 }
@@ -102,7 +101,7 @@ BlockPlan grouped_plan(const dqgemm_s* h, int M) {
   BlockPlan pl{};
   const long long mean = ceil_div(M, h->E);
   pl.pair = mean > 160;
-  pl.bn = pl.pair ? 256 : M <= 16 ? 16 : mean <= 16 ? 32 : mean <= 48 ? 64 : 128;
+  pl.bn = pl.pair ? 256 : M <= 16 || mean <= 4 ? 16 : mean <= 16 ? 32 : mean <= 48 ? 64 : 128;
   pl.n_tiles = (int)ceil_div(h->N, pl.pair ? 256 : 128);
   pl.m_tiles = 0;
   pl.split = 1;
@@ -165,27 +164,46 @@ cudaError_t launch(K kern, int grid, int threads, int smem, int cluster, const C
   return cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
 }
 
+template <int BN, bool G, bool X>
+cudaError_t launch_skinny(const BlockPlan& pl, const CUtensorMap& tw, const CUtensorMap& tx, const BlockParams& p,
+                          cudaStream_t s) {
+  using C = SkinnyCfg<BN, X>;
+  return launch(block_skinny_kernel<BN, G, X>, pl.grid, C::THREADS, C::SMEM, pl.split, tw, tx, p, s);
+}
+
 template <bool G>
 cudaError_t launch_plan(const BlockPlan& pl, const CUtensorMap& tw, const CUtensorMap& tx, const BlockParams& p,
                         cudaStream_t s) {
   // (the pair kernel's cluster size is a property of the kernel)
   if (pl.pair) return launch(block_pair_kernel<G>, pl.grid, PairCfg::THREADS, PairCfg::SMEM, 1, tw, tx, p, s);
+  if (p.x) return launch_skinny<16, G, true>(pl, tw, tx, p, s);
   switch (pl.bn) {
-    case 16: return launch(block_skinny_kernel<16, G>, pl.grid, 384, SkinnyCfg<16>::SMEM, pl.split, tw, tx, p, s);
-    case 32: return launch(block_skinny_kernel<32, G>, pl.grid, 384, SkinnyCfg<32>::SMEM, pl.split, tw, tx, p, s);
-    case 64: return launch(block_skinny_kernel<64, G>, pl.grid, 384, SkinnyCfg<64>::SMEM, pl.split, tw, tx, p, s);
-    default: return launch(block_skinny_kernel<128, G>, pl.grid, 384, SkinnyCfg<128>::SMEM, pl.split, tw, tx, p, s);
+    case 16: return launch_skinny<16, G, false>(pl, tw, tx, p, s);
+    case 32: return launch_skinny<32, G, false>(pl, tw, tx, p, s);
+    case 64: return launch_skinny<64, G, false>(pl, tw, tx, p, s);
+    default: return launch_skinny<128, G, false>(pl, tw, tx, p, s);
   }
 }
 
-// arguments checked by the callers
-dqgemm_status run_codes(dqgemm_handle h, const void* q, const float* sx, int M, const int* offsets, void* y, void* stream) {
-  const BlockPlan pl = offsets ? grouped_plan(h, M) : dense_plan(h, M);
+// Whether a call on bf16 activations quantizes them in the product itself: up
+// to 8 rows (experts: 16, or 4 an expert on the mean), which the quantizing
+// warps handle within the weight's stream.  Beyond, quantizing them once ahead
+// is faster: 1 x 4096 x 14336 14.9 us either way, but 16 rows 20.5 against 15.3.
+bool quantizes(const dqgemm_s* h, int M, bool grouped) {
+  return grouped ? M <= 16 || M <= 4 * h->E : M <= 8;
+}
+
+// Codes q and scales sx, or (where quantizes(plan)) bf16 x; arguments checked
+// by the callers.
+dqgemm_status run_block(dqgemm_handle h, const BlockPlan& pl, const void* q, const float* sx, const void* x, int M,
+                        const int* offsets, void* y, void* stream) {
   if ((M / pl.bn + (long long)std::max(h->E, 1)) * pl.n_tiles > 0x7FFFFFFFll) return DQ_ERR_UNSUPPORTED;
+  const CUtensorMap& tw = pl.pair ? h->wmap64 : h->wmap;
   CUtensorMap tx;
-  if (!codes_map(h, q, M, pl.pair ? 128 : pl.bn, &tx)) return DQ_ERR_CUDA;
+  if (!x && !codes_map(h, q, M, pl.pair ? 128 : pl.bn, &tx)) return DQ_ERR_CUDA;
   BlockParams p{};
   p.sx = sx;
+  p.x = static_cast<const __nv_bfloat16*>(x);
   p.sw = h->col_scale;
   p.bias = h->bias;
   p.y = static_cast<__nv_bfloat16*>(y);
@@ -193,6 +211,7 @@ dqgemm_status run_codes(dqgemm_handle h, const void* q, const float* sx, int M, 
   p.status = h->status;
   p.M = M;
   p.N = h->N;
+  p.K = h->K;
   p.E = h->E;
   p.kb = h->k_stages;
   p.nb = h->n_tiles;
@@ -203,8 +222,22 @@ dqgemm_status run_codes(dqgemm_handle h, const void* q, const float* sx, int M, 
   p.timeout_ns = h->timeout_ns;
   p.drain_ns = std::max(timeout_ns(), kDefaultTimeoutNs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const CUtensorMap& tw = pl.pair ? h->wmap64 : h->wmap;
-  return cuda_err(offsets ? launch_plan<true>(pl, tw, tx, p, s) : launch_plan<false>(pl, tw, tx, p, s));
+  // (a call on bf16 x uses no map of the codes: any map fills the parameter)
+  return cuda_err(offsets ? launch_plan<true>(pl, tw, x ? tw : tx, p, s) : launch_plan<false>(pl, tw, x ? tw : tx, p, s));
+}
+
+long long x_workspace(const dqgemm_s* h, int M, bool grouped) {
+  return quantizes(h, M, grouped) ? 0 : ((long long)M * h->K + 255) / 256 * 256 + (long long)M * h->k_stages * 4;
+}
+
+// x bf16: in one launch where the product quantizes it itself, else quantized
+// into the workspace `ws` (codes, then scales) first
+dqgemm_status run_x(dqgemm_handle h, const void* x, int M, const int* offsets, void* y, void* ws, void* stream) {
+  const BlockPlan pl = offsets ? grouped_plan(h, M) : dense_plan(h, M);
+  if (quantizes(h, M, offsets != nullptr)) return run_block(h, pl, nullptr, nullptr, x, M, offsets, y, stream);
+  float* sx = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)M * h->K + 255) / 256 * 256);
+  const dqgemm_status st = dqgemm_quantize_act_fp8_block(DQ_BF16, x, h->K, M, h->K, ws, sx, stream);
+  return st == DQ_OK ? run_block(h, pl, ws, sx, nullptr, M, offsets, y, stream) : st;
 }
 
 }  // namespace
@@ -267,11 +300,11 @@ dqgemm_status block_create(dqgemm_handle* out, int E, int K, int N, const void* 
   return DQ_OK;
 }
 
-// x bf16: quantized into the handle's workspace (codes, then scales), then the product
+// dqgemm_run: the workspace, where one is needed, is the handle's
 dqgemm_status block_run_x(dqgemm_handle h, const void* x, int M, void* y, void* stream) {
   if (!aligned16(x) || !aligned16(y)) return DQ_ERR_ALIGNMENT;
-  const size_t qb = ((size_t)M * h->K + 255) / 256 * 256, total = qb + (size_t)M * h->k_stages * 4;
-  {
+  const size_t total = (size_t)x_workspace(h, M, false);
+  if (total > 0) {
     std::lock_guard<std::mutex> lock(h->maps_mu);
     if (h->ws_bytes < total) {
       // grow: calls already launched may still read the old workspace
@@ -279,7 +312,6 @@ dqgemm_status block_run_x(dqgemm_handle h, const void* x, int M, void* y, void* 
       cudaFree(h->ws);
       h->ws = nullptr;
       h->ws_bytes = 0;
-      for (auto& m : h->maps) m.x = nullptr;
       if (cudaMalloc(&h->ws, total) != cudaSuccess) {
         cudaGetLastError();
         h->ws = nullptr;
@@ -288,9 +320,7 @@ dqgemm_status block_run_x(dqgemm_handle h, const void* x, int M, void* y, void* 
       h->ws_bytes = total;
     }
   }
-  float* sx = reinterpret_cast<float*>(h->ws + qb);
-  const dqgemm_status st = dqgemm_quantize_act_fp8_block(DQ_BF16, x, h->K, M, h->K, h->ws, sx, stream);
-  return st == DQ_OK ? run_codes(h, h->ws, sx, M, nullptr, y, stream) : st;
+  return run_x(h, x, M, nullptr, y, h->ws, stream);
 }
 
 dqgemm_status block_dequantize(dqgemm_handle h, void* w_bf16, void* stream) {
@@ -309,16 +339,16 @@ void block_fill_plan(dqgemm_handle h, int M, dqgemm_plan* pl) {
   pl->grid = b.grid;
   pl->max_segments = b.split;
   pl->stages = pl->x_stages = b.pair ? PairCfg::ST
-                              : b.bn == 16 ? SkinnyCfg<16>::ST
-                              : b.bn == 32 ? SkinnyCfg<32>::ST
-                              : b.bn == 64 ? SkinnyCfg<64>::ST
-                                           : SkinnyCfg<128>::ST;
+                              : b.bn == 16 ? SkinnyCfg<16, true>::ST
+                              : b.bn == 32 ? SkinnyCfg<32, false>::ST
+                              : b.bn == 64 ? SkinnyCfg<64, false>::ST
+                                           : SkinnyCfg<128, false>::ST;
   pl->smem_bytes = b.pair ? PairCfg::SMEM
-                   : b.bn == 16 ? SkinnyCfg<16>::SMEM
-                   : b.bn == 32 ? SkinnyCfg<32>::SMEM
-                   : b.bn == 64 ? SkinnyCfg<64>::SMEM
-                                : SkinnyCfg<128>::SMEM;
-  pl->workspace_bytes = h->E > 1 ? 0 : ((long long)M * h->K + 255) / 256 * 256 + (long long)M * h->k_stages * 4;
+                   : b.bn == 16 ? SkinnyCfg<16, true>::SMEM
+                   : b.bn == 32 ? SkinnyCfg<32, false>::SMEM
+                   : b.bn == 64 ? SkinnyCfg<64, false>::SMEM
+                                : SkinnyCfg<128, false>::SMEM;
+  pl->workspace_bytes = x_workspace(h, M, h->E > 1);
   pl->weight_bytes = h->weight_bytes;
   const long long T = (long long)pl->m_tiles * b.n_tiles;
   const long long at_once = b.pair ? b.grid / 2 : b.grid;
@@ -369,7 +399,7 @@ dqgemm_status dqgemm_run_fp8_block_quantized(dqgemm_handle h, const void* q, con
   if (!h || !q || !scales || !y || M < 1) return DQ_ERR_INVALID_ARG;
   if (h->fmt != FMT_FP8B || h->E != 1) return DQ_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(y) || reinterpret_cast<uintptr_t>(scales) % 4) return DQ_ERR_ALIGNMENT;
-  return run_codes(h, q, scales, M, nullptr, y, stream);
+  return run_block(h, dense_plan(h, M), q, scales, nullptr, M, nullptr, y, stream);
 }
 
 dqgemm_status dqgemm_run_experts_quantized(dqgemm_handle h, const void* q, const float* scales, int M, const int* offsets,
@@ -379,7 +409,18 @@ dqgemm_status dqgemm_run_experts_quantized(dqgemm_handle h, const void* q, const
   if (!aligned16(q) || !aligned16(y) || reinterpret_cast<uintptr_t>(scales) % 4 ||
       reinterpret_cast<uintptr_t>(offsets) % 4)
     return DQ_ERR_ALIGNMENT;
-  return run_codes(h, q, scales, M, offsets, y, stream);
+  return run_block(h, grouped_plan(h, M), q, scales, nullptr, M, offsets, y, stream);
+}
+
+dqgemm_status dqgemm_run_fp8_block(dqgemm_handle h, const void* x, int M, const int* offsets, void* y, void* workspace,
+                                   long long workspace_bytes, void* stream) {
+  if (!h || !x || !y || M < 1) return DQ_ERR_INVALID_ARG;
+  if (h->fmt != FMT_FP8B || (!offsets && h->E != 1)) return DQ_ERR_UNSUPPORTED;
+  const long long need = x_workspace(h, M, offsets != nullptr);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return DQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y) || (need > 0 && !aligned16(workspace)) || reinterpret_cast<uintptr_t>(offsets) % 4)
+    return DQ_ERR_ALIGNMENT;
+  return run_x(h, x, M, offsets, y, workspace, stream);
 }
 
 }  // extern "C"

@@ -127,6 +127,38 @@ __device__ __forceinline__ void load8_typed(const void* p, int type, long long a
 // quantization to e4m3
 // ---------------------------------------------------------------------------
 
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The scale of a block, s = f32(amax / 448), and r = f32(1 / s) (1 for s = 0),
+// from the bits of amax.  Straight-line: both quotients by Markstein's
+// correction steps (see e4m3_quotient), r from the hardware's reciprocal
+// (within 2^-23) by one step, which gives the correctly rounded value unless
+// s has the largest significand.  `fast` says that s and r are what they
+// should be and that r is a normal number: amax is 0, or from 2^-87 to the
+// largest finite value, and s has another significand.  The division's own
+// code has branches for special operands (zero among them, the commonest
+// block of all) that keep several blocks from being worked on at once.
+struct BlockScale {
+  float s, r;
+  bool fast;
+};
+__device__ __forceinline__ BlockScale block_scale_of(uint32_t amax_bits) {
+  constexpr float r448 = 1.f / 448.f;
+  const float a = __uint_as_float(amax_bits);
+  const float q0 = __fmul_rn(a, r448);
+  BlockScale b;
+  b.s = __fmaf_rn(__fmaf_rn(-q0, 448.f, a), r448, q0);
+  const float d = amax_bits == 0u ? 1.f : b.s;
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+  b.r = __fmaf_rn(y, __fmaf_rn(-d, y, 1.f), y);
+  b.fast = amax_bits == 0u || (amax_bits - 0x14000000u < 0x7F800000u - 0x14000000u &&
+                               (__float_as_uint(b.s) & 0x7FFFFFu) != 0x7FFFFFu);
+  return b;
+}
+
 // f32(v / s), correctly rounded where the e4m3 code depends on it, without
 // the range test of e4m3_quotient: for r = f32(1 / s) normal and |v / s| not
 // above 2^9, the correction leaves every quotient below 2^-12 there (where
@@ -137,42 +169,46 @@ __device__ __forceinline__ float block_quotient(float v, float s, float r) {
   return __uint_as_float((__float_as_uint(q) & 0x7FFFFFFFu) | (__float_as_uint(v) & 0x80000000u));
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+// The 8 codes of v under the scale s: e4m3(f32(v / s)), 0 where s is 0; for
+// blocks whose scale is `fast` ...
+__device__ __forceinline__ uint2 codes8_fast(const float (&v)[8], float s, float r) {
+  const uint32_t lo = e4m3x2(block_quotient(v[0], s, r), block_quotient(v[1], s, r)) |
+                      (e4m3x2(block_quotient(v[2], s, r), block_quotient(v[3], s, r)) << 16);
+  const uint32_t hi = e4m3x2(block_quotient(v[4], s, r), block_quotient(v[5], s, r)) |
+                      (e4m3x2(block_quotient(v[6], s, r), block_quotient(v[7], s, r)) << 16);
+  return s == 0.f ? make_uint2(0u, 0u) : make_uint2(lo, hi);
 }
-
-// The 8 codes of v under the scale s: e4m3(f32(v / s)), 0 where s is 0.  A
-// scale outside the normal range of its reciprocal (a NaN or infinite one
-// too: every code of its block is then NaN, or 0 for the finite elements of
-// an infinite block) goes through the division itself.
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
-  const float r = __frcp_rn(s);
-  uint32_t lo, hi;
-  if (e4m3_quotient_ok(r)) {
-    lo = e4m3x2(block_quotient(v[0], s, r), block_quotient(v[1], s, r)) |
-         (e4m3x2(block_quotient(v[2], s, r), block_quotient(v[3], s, r)) << 16);
-    hi = e4m3x2(block_quotient(v[4], s, r), block_quotient(v[5], s, r)) |
-         (e4m3x2(block_quotient(v[6], s, r), block_quotient(v[7], s, r)) << 16);
-  } else if (s == 0.f) {
-    lo = hi = 0u;
-  } else {
-    lo = e4m3x2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)) | (e4m3x2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)) << 16);
-    hi = e4m3x2(__fdiv_rn(v[4], s), __fdiv_rn(v[5], s)) | (e4m3x2(__fdiv_rn(v[6], s), __fdiv_rn(v[7], s)) << 16);
-  }
+// ... and for any scale, by the division (a NaN makes every code of its block
+// NaN; in a block with an infinity the finite elements' codes are 0)
+static __device__ __noinline__ uint2 codes8_any(const float (&v)[8], float s) {
+  if (s == 0.f) return make_uint2(0u, 0u);
+  const uint32_t lo = e4m3x2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)) | (e4m3x2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)) << 16);
+  const uint32_t hi = e4m3x2(__fdiv_rn(v[4], s), __fdiv_rn(v[5], s)) | (e4m3x2(__fdiv_rn(v[6], s), __fdiv_rn(v[7], s)) << 16);
   return make_uint2(lo, hi);
 }
 
-// The scale of the 128 elements that 16 neighbouring lanes hold: f32(amax /
-// 448).  The maximum is taken over the magnitudes' bits, whose order is the
-// values' with NaN above infinity, so a NaN makes the scale NaN.  The whole
-// warp calls this.
-__device__ __forceinline__ float block_scale(const float (&v)[8]) {
+// Bits of the largest magnitude of the 128 elements that 16 neighbouring lanes
+// hold.  The bits' order is the values', with NaN above infinity, so a NaN
+// makes the scale NaN.  The whole warp calls this.
+__device__ __forceinline__ uint32_t block_amax(const float (&v)[8]) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
 #pragma unroll
   for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return __fdiv_rn(__uint_as_float(m), 448.f);
+  return m;
+}
+
+// scale and codes of a warp's two blocks (the whole warp calls this)
+__device__ __forceinline__ uint2 quantize_block(const float (&v)[8], float* s) {
+  const uint32_t m = block_amax(v);
+  const BlockScale b = block_scale_of(m);
+  if (__all_sync(0xFFFFFFFFu, b.fast)) {
+    *s = b.s;
+    return codes8_fast(v, b.s, b.r);
+  }
+  *s = __fdiv_rn(__uint_as_float(m), 448.f);
+  return codes8_any(v, *s);
 }
 
 template <bool AL>
@@ -193,10 +229,11 @@ template <int OUT, bool AL>
 __device__ __forceinline__ void emit8(const RowArgs& a, int row, int vec, int n, const float (&v)[8]) {
   const long long at = (long long)row * a.K + vec * 8;
   if constexpr (OUT == OUT_BLOCK) {
-    const float s = block_scale(v);
+    float s;
+    const uint2 c = quantize_block(v, &s);
     if (n > 0) {
       if ((vec & 15) == 0) a.scales[(long long)row * ((a.K + QBLOCK - 1) / QBLOCK) + (vec >> 4)] = s;
-      store_codes<AL>(static_cast<uint8_t*>(a.out) + at, n, codes8(v, s));
+      store_codes<AL>(static_cast<uint8_t*>(a.out) + at, n, c);
     }
   } else if constexpr (OUT == OUT_STATIC) {
     uint32_t w[2];
