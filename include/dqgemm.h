@@ -308,8 +308,9 @@ dqgemm_status dqgemm_quantize_act_fp4(dqgemm_format fmt, const void* x, int M, i
  *   DQ_OUT_FP8_STATIC           out u8 [M, K]: e4m3(f32(v / s_out)),
  *       saturating, the codes that a DQ_FP8_STATIC layer calibrated with
  *       s_out takes (dqgemm_run_fp8_static_quantized); s_out finite and > 0
- * Buffers need their natural alignment only; 16-byte aligned rows (8-byte
- * for codes) are moved in vectors, others element by element.
+ * Buffers need their natural alignment only; rows aligned to 32 bytes (16 for
+ * codes) with K % 16 == 0, or to half of that with K % 8 == 0, are moved in
+ * vectors, others element by element.
  * M >= 1, 1 <= K <= 2^28.  One launch on `stream`, no allocation, no
  * synchronization; programmatic dependent launch as dqgemm_run, and nothing
  * is read or written before the previous kernel of the stream has completed. */

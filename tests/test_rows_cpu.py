@@ -6,7 +6,7 @@ import torch
 
 import weight_only_quantized_prologue_b200 as dq
 
-BAD, ALIGN, UNSUP = dq._native.DQ_ERR_INVALID_ARG, dq._native.DQ_ERR_ALIGNMENT, dq._native.DQ_ERR_UNSUPPORTED
+BAD, ALIGN = dq._native.DQ_ERR_INVALID_ARG, dq._native.DQ_ERR_ALIGNMENT
 NAN, INF = float("nan"), float("inf")
 
 
@@ -47,7 +47,7 @@ def test_silu_mul_and_quantizer_refuse_bad_arguments():
     assert lib.dqgemm_silu_mul(0, 64, 512, 2, 256, 3, 1.0, 64, None, None) == BAD
     assert lib.dqgemm_silu_mul(0, 64, 512, 2, 256, 4, -1.0, 64, None, None) == BAD
     assert lib.dqgemm_silu_mul(2, 66, 512, 2, 256, 0, 1.0, 64, None, None) == ALIGN
-    assert lib.dqgemm_silu_mul(0, 64, 1 << 29, (1 << 31) - 1, 1 << 20, 0, 1.0, 64, None, None) == UNSUP
+    assert lib.dqgemm_silu_mul(0, 64, 1 << 30, 2, 1 << 29, 0, 1.0, 64, None, None) == BAD
     assert lib.dqgemm_quantize_act_fp8_block(0, 64, 256, 2, 256, 64, None, None) == BAD
     assert lib.dqgemm_quantize_act_fp8_block(0, 64, 256, 2, 256, None, 64, None) == BAD
     assert lib.dqgemm_quantize_act_fp8_block(0, 64, 100, 2, 256, 64, 64, None) == BAD

@@ -4,10 +4,14 @@
 // e4m3 codes with an fp32 scale per 128 elements of a row, or as e4m3 codes
 // under one given scale.  All arithmetic is fp32.
 //
-// All of them are bound by HBM: each input is read once and each output
-// written once.  A thread works on vectors of 8 consecutive elements (one
-// 16-byte load in 16 bits, one 8-byte store of codes), and 16 neighbouring
-// lanes hold one block of 128, so a block's maximum is four shuffles.
+// All of them read each input once and write each output once.  At the rate of
+// HBM that leaves about 27 instructions per element of a gated SiLU, so the
+// kernels are written for few of them: a thread works on vectors of 16
+// consecutive elements (one 32-byte load in 16 bits, one 16-byte store of
+// codes), 8 neighbouring lanes hold one block of 128, and what a block costs
+// (three shuffles, its scale and reciprocal) is shared by 16 elements a lane.
+// With 8 elements a lane the quantizer took 20 instructions an element and
+// was bound by their issue (67 to 81 % of the slots, 45 to 70 % of HBM).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,9 +41,10 @@ struct RowArgs {
 };
 
 // ---------------------------------------------------------------------------
-// 8 consecutive elements <-> fp32.  AL: rows are 16-byte aligned and K a
-// multiple of 8, so a vector is whole; else n of its elements exist (n <= 0:
-// none) and they are taken one by one.  Missing elements read as 0.
+// 16 consecutive elements <-> fp32, n of which exist (n <= 0: none); missing
+// ones read as 0.  AL = 2: rows are 32-byte aligned and K is a multiple of 16,
+// so a vector is whole; 1: 16-byte aligned and a multiple of 8, so each half
+// is; 0: element by element.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -69,58 +74,110 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, __half) 
   b = __high2float(h);
 }
 
-template <bool AL, typename T>
-__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
-  if constexpr (AL) {
-    if (n > 0) {
-      if constexpr (sizeof(T) == 2) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        unpack2(u.x, v[0], v[1], T());
-        unpack2(u.y, v[2], v[3], T());
-        unpack2(u.z, v[4], v[5], T());
-        unpack2(u.w, v[6], v[7], T());
+// 32 bytes in one instruction (sm_100), in program order with the stores
+__device__ __forceinline__ void ld32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// a vector as it lies in memory (AL = 0: its elements' bits one a word)
+template <int AL, typename T>
+struct Raw16 {
+  static constexpr int WORDS = AL == 0 ? 16 : 4 * sizeof(T);
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if constexpr (AL == 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = i < n ? bits(p[i]) : 0u;
+    } else if constexpr (AL == 2) {
+      if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 8) ld32(reinterpret_cast<const uint32_t*>(p) + i, *reinterpret_cast<uint32_t(*)[8]>(w + i));
       } else {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
-  }
-}
-
-template <bool AL, typename T>
-__device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
-  if constexpr (AL) {
-    if (n > 0) {
-      if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
-                                                  pack2<T>(v[6], v[7]));
-      } else {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      for (int i = 0; i < WORDS; i += 4) {
+        const uint4 u = (i < WORDS / 2 ? n > 0 : n > 8) ? reinterpret_cast<const uint4*>(p)[i / 4] : make_uint4(0u, 0u, 0u, 0u);
+        w[i] = u.x;
+        w[i + 1] = u.y;
+        w[i + 2] = u.z;
+        w[i + 3] = u.w;
       }
     }
-  } else {
+  }
+  __device__ __forceinline__ void values(float (&v)[16]) const {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (AL == 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint16_t h = (uint16_t)w[i];
+        v[i] = to_f32(*reinterpret_cast<const T*>(&h));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) unpack2(w[i], v[2 * i], v[2 * i + 1], T());
+    }
+  }
+  static __device__ __forceinline__ uint32_t bits(T v) {
+    if constexpr (sizeof(T) == 4) return *reinterpret_cast<const uint32_t*>(&v);
+    else return *reinterpret_cast<const uint16_t*>(&v);
+  }
+};
+
+template <int AL, typename T>
+__device__ __forceinline__ void load16(const T* p, int n, float (&v)[16]) {
+  Raw16<AL, T> raw;
+  raw.load(p, n);
+  raw.values(v);
+}
+
+template <int AL, typename T>
+__device__ __forceinline__ void store16(T* p, int n, const float (&v)[16]) {
+  if constexpr (AL == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
       if (i < n) p[i] = from_f32<T>(v[i]);
+  } else {
+    constexpr int WORDS = 4 * sizeof(T);
+    uint32_t w[WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(T) == 2) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+      else w[i] = __float_as_uint(v[i]);
+    }
+    if constexpr (AL == 2) {
+      if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 8) st32(reinterpret_cast<uint32_t*>(p) + i, *reinterpret_cast<uint32_t(*)[8]>(w + i));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < WORDS; i += 4)
+        if (i < WORDS / 2 ? n > 0 : n > 8) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
   }
 }
 
-template <bool AL>
-__device__ __forceinline__ void load8_typed(const void* p, int type, long long at, int n, float (&v)[8]) {
+template <int AL>
+__device__ __forceinline__ void load16_typed(const void* p, int type, long long at, int n, float (&v)[16]) {
   if (type == ROW_BF16)
-    load8<AL>(static_cast<const __nv_bfloat16*>(p) + at, n, v);
+    load16<AL>(static_cast<const __nv_bfloat16*>(p) + at, n, v);
   else if (type == ROW_FP16)
-    load8<AL>(static_cast<const __half*>(p) + at, n, v);
+    load16<AL>(static_cast<const __half*>(p) + at, n, v);
   else
-    load8<AL>(static_cast<const float*>(p) + at, n, v);
+    load16<AL>(static_cast<const float*>(p) + at, n, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -162,16 +219,16 @@ __device__ __forceinline__ BlockScale block_scale_of(uint32_t amax_bits) {
 // f32(v / s), correctly rounded where the e4m3 code depends on it, without
 // the range test of e4m3_quotient: for r = f32(1 / s) normal and |v / s| not
 // above 2^9, the correction leaves every quotient below 2^-12 there (where
-// each code is 0) and cannot overflow.  The sign is v's, of a zero too.
+// each code is 0) and cannot overflow.  The remainder is taken negated, so
+// that a zero keeps its sign through both steps.
 __device__ __forceinline__ float block_quotient(float v, float s, float r) {
   const float q0 = __fmul_rn(v, r);
-  const float q = __fmaf_rn(__fmaf_rn(-q0, s, v), r, q0);
-  return __uint_as_float((__float_as_uint(q) & 0x7FFFFFFFu) | (__float_as_uint(v) & 0x80000000u));
+  return __fmaf_rn(-__fmaf_rn(q0, s, -v), r, q0);
 }
 
 // The 8 codes of v under the scale s: e4m3(f32(v / s)), 0 where s is 0; for
 // blocks whose scale is `fast` ...
-__device__ __forceinline__ uint2 codes8_fast(const float (&v)[8], float s, float r) {
+__device__ __forceinline__ uint2 codes8_fast(const float* v, float s, float r) {
   const uint32_t lo = e4m3x2(block_quotient(v[0], s, r), block_quotient(v[1], s, r)) |
                       (e4m3x2(block_quotient(v[2], s, r), block_quotient(v[3], s, r)) << 16);
   const uint32_t hi = e4m3x2(block_quotient(v[4], s, r), block_quotient(v[5], s, r)) |
@@ -180,76 +237,91 @@ __device__ __forceinline__ uint2 codes8_fast(const float (&v)[8], float s, float
 }
 // ... and for any scale, by the division (a NaN makes every code of its block
 // NaN; in a block with an infinity the finite elements' codes are 0)
-static __device__ __noinline__ uint2 codes8_any(const float (&v)[8], float s) {
-  if (s == 0.f) return make_uint2(0u, 0u);
-  const uint32_t lo = e4m3x2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)) | (e4m3x2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)) << 16);
-  const uint32_t hi = e4m3x2(__fdiv_rn(v[4], s), __fdiv_rn(v[5], s)) | (e4m3x2(__fdiv_rn(v[6], s), __fdiv_rn(v[7], s)) << 16);
-  return make_uint2(lo, hi);
+__device__ __forceinline__ uint2 codes8_any(const float* v, float s) {
+  uint32_t w[2] = {0u, 0u};
+  if (s != 0.f) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const float a = h ? v[4] : v[0], b = h ? v[5] : v[1], c = h ? v[6] : v[2], d = h ? v[7] : v[3];
+      const uint32_t x = e4m3x2(__fdiv_rn(a, s), __fdiv_rn(b, s)) | (e4m3x2(__fdiv_rn(c, s), __fdiv_rn(d, s)) << 16);
+      if (h) w[1] = x;
+      else w[0] = x;
+    }
+  }
+  return make_uint2(w[0], w[1]);
 }
 
-// Bits of the largest magnitude of the 128 elements that 16 neighbouring lanes
-// hold.  The bits' order is the values', with NaN above infinity, so a NaN
-// makes the scale NaN.  The whole warp calls this.
-__device__ __forceinline__ uint32_t block_amax(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return m;
+// the larger magnitude, NaN if either is
+__device__ __forceinline__ float amax2(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
-// scale and codes of a warp's two blocks (the whole warp calls this)
-__device__ __forceinline__ uint2 quantize_block(const float (&v)[8], float* s) {
-  const uint32_t m = block_amax(v);
-  const BlockScale b = block_scale_of(m);
+// Scale and codes of a warp's four blocks, 8 lanes each (the whole warp calls
+// this).  A NaN makes the maximum and so the scale NaN.
+__device__ __forceinline__ uint4 quantize_block(const float (&v)[16], float* s) {
+  float a = amax2(amax2(amax2(amax2(v[0], v[1]), amax2(v[2], v[3])), amax2(amax2(v[4], v[5]), amax2(v[6], v[7]))),
+                  amax2(amax2(amax2(v[8], v[9]), amax2(v[10], v[11])), amax2(amax2(v[12], v[13]), amax2(v[14], v[15]))));
+#pragma unroll
+  for (int o = 4; o; o >>= 1) a = amax2(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+  const BlockScale b = block_scale_of(__float_as_uint(a));
+  uint2 lo, hi;
   if (__all_sync(0xFFFFFFFFu, b.fast)) {
     *s = b.s;
-    return codes8_fast(v, b.s, b.r);
-  }
-  *s = __fdiv_rn(__uint_as_float(m), 448.f);
-  return codes8_any(v, *s);
-}
-
-template <bool AL>
-__device__ __forceinline__ void store_codes(uint8_t* p, int n, uint2 c) {
-  if constexpr (AL) {
-    if (n > 0) *reinterpret_cast<uint2*>(p) = c;
+    lo = codes8_fast(v, b.s, b.r);
+    hi = codes8_fast(v + 8, b.s, b.r);
   } else {
+    *s = __fdiv_rn(a, 448.f);
+    lo = codes8_any(v, *s);
+    hi = codes8_any(v + 8, *s);
+  }
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+
+template <int AL>
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, uint4 c) {
+  if constexpr (AL == 2) {
+    if (n > 0) *reinterpret_cast<uint4*>(p) = c;
+  } else if constexpr (AL == 1) {
+    if (n > 0) *reinterpret_cast<uint2*>(p) = make_uint2(c.x, c.y);
+    if (n > 8) *reinterpret_cast<uint2*>(p + 8) = make_uint2(c.z, c.w);
+  } else {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
 }
 
-// Vector `vec` (8 elements) of row `row`, n of which exist, to the output.
+// Vector `vec` (16 elements) of row `row`, n of which exist, to the output.
 // The whole warp calls this, its lanes holding consecutive vectors from a
 // multiple of 32 on.
-template <int OUT, bool AL>
-__device__ __forceinline__ void emit8(const RowArgs& a, int row, int vec, int n, const float (&v)[8]) {
-  const long long at = (long long)row * a.K + vec * 8;
+template <int OUT, int AL>
+__device__ __forceinline__ void emit16(const RowArgs& a, int row, int vec, int n, const float (&v)[16]) {
+  const long long at = (long long)row * a.K + vec * 16;
   if constexpr (OUT == OUT_BLOCK) {
     float s;
-    const uint2 c = quantize_block(v, &s);
+    const uint4 c = quantize_block(v, &s);
     if (n > 0) {
-      if ((vec & 15) == 0) a.scales[(long long)row * ((a.K + QBLOCK - 1) / QBLOCK) + (vec >> 4)] = s;
+      if ((vec & 7) == 0) a.scales[(long long)row * ((a.K + QBLOCK - 1) / QBLOCK) + (vec >> 3)] = s;
       store_codes<AL>(static_cast<uint8_t*>(a.out) + at, n, c);
     }
   } else if constexpr (OUT == OUT_STATIC) {
-    uint32_t w[2];
+    uint32_t w[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 4; ++h) {
       w[h] = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[h] |= (uint32_t)act_code_r(v[4 * h + i], a.s_out, a.r_out) << (8 * i);
     }
-    store_codes<AL>(static_cast<uint8_t*>(a.out) + at, n, make_uint2(w[0], w[1]));
+    store_codes<AL>(static_cast<uint8_t*>(a.out) + at, n, make_uint4(w[0], w[1], w[2], w[3]));
   } else if constexpr (OUT == OUT_BF16) {
-    store8<AL>(static_cast<__nv_bfloat16*>(a.out) + at, n, v);
+    store16<AL>(static_cast<__nv_bfloat16*>(a.out) + at, n, v);
   } else if constexpr (OUT == OUT_FP16) {
-    store8<AL>(static_cast<__half*>(a.out) + at, n, v);
+    store16<AL>(static_cast<__half*>(a.out) + at, n, v);
   } else {
-    store8<AL>(static_cast<float*>(a.out) + at, n, v);
+    store16<AL>(static_cast<float*>(a.out) + at, n, v);
   }
 }
 
@@ -257,8 +329,9 @@ __device__ __forceinline__ void emit8(const RowArgs& a, int row, int vec, int n,
 // RMS norm:  r = x + residual,  y = r * w / sqrt(mean(r^2) + eps).
 // The sum r is kept in fp32 for the norm (only the residual that is stored is
 // rounded), so the output carries one rounding.  blockDim.x threads hold a
-// row (NV vectors each, read once) and blockDim.y rows share a CTA; NV = 0
-// reads the row twice, for rows that do not fit in registers.
+// row (NV vectors each, read once) and blockDim.y rows share a CTA, which
+// goes on to the next rows with their loads already under way and the weight
+// kept in registers.  NV = 0 reads the row twice, for rows that do not fit.
 // residual_out may be the residual or x itself: every element is read by the
 // thread that writes it, before it is written.
 // ---------------------------------------------------------------------------
@@ -276,85 +349,120 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-template <typename T, int NV, int OUT, bool AL>
+template <typename T, int NV, int OUT, int AL>
 __global__ void __launch_bounds__(512) rmsnorm_kernel(const RowArgs a) {
-  __shared__ float part[16];
+  __shared__ float part[2][16];   // in turn, so that one barrier a row will do
   pdl_launch_dependents();
   pdl_wait();   // x, the residual and the weight may be the previous grid's output
-  const int row_raw = blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = row_raw < a.M;
-  const int row = live ? row_raw : 0;
   const int K = a.K;
-  const T* x = static_cast<const T*>(a.x) + (long long)row * a.ldx;
-  const T* res = a.res ? static_cast<const T*>(a.res) + (long long)row * K : nullptr;
-  T* res_out = a.res ? static_cast<T*>(a.res_out) + (long long)row * K : nullptr;
-  const auto load = [&](int vec, int n, float (&r)[8]) {
-    load8<AL>(x + vec * 8, n, r);
-    if (res) {
-      float b[8];
-      load8<AL>(res + vec * 8, n, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] += b[i];
-    }
-  };
-  const auto finish = [&](int vec, int n, float rs, float (&r)[8]) {
-    float w[8];
-    if (a.w) {
-      load8_typed<AL>(a.w, a.w_type, vec * 8, n, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = r[i] * rs * w[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] *= rs;
-    }
-    emit8<OUT, AL>(a, row, vec, n, r);
-  };
-  float sum = 0.f;
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.res);
+  T* res_out = static_cast<T*>(a.res_out);
+  const int step = gridDim.x * blockDim.y;
   if constexpr (NV > 0) {
-    float r[NV][8];
+    const auto count = [&](long long row, int i) {
+      return row < a.M ? K - ((int)threadIdx.x + i * (int)blockDim.x) * 16 : 0;
+    };
+    Raw16<AL, T> cx[NV], cr[NV];
+    const auto fetch = [&](long long row) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int vec = threadIdx.x + i * blockDim.x, n = count(row, i);
+        cx[i].load(x + row * a.ldx + vec * 16, n);
+        if (res) cr[i].load(res + row * K + vec * 16, n);
+      }
+    };
+    long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    fetch(row);
+    float w[NV][16];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int vec = threadIdx.x + i * blockDim.x;
-      const int n = live ? K - vec * 8 : 0;
-      load(vec, n, r[i]);
+      if (a.w) {
+        load16_typed<AL>(a.w, a.w_type, vec * 16, K - vec * 16, w[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[i][j] = 1.f;
+      }
     }
+    int turn = 0;
+    // (the bound is of the CTA's first row: its threads meet in row_sum)
+    for (long long first = (long long)blockIdx.x * blockDim.y; first < a.M; first += step, row += step, turn ^= 1) {
+      float r[NV][16];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int vec = threadIdx.x + i * blockDim.x;
-      const int n = live ? K - vec * 8 : 0;
-      if (res_out) store8<AL>(res_out + vec * 8, n, r[i]);
+      for (int i = 0; i < NV; ++i) {
+        cx[i].values(r[i]);
+        if (res) {
+          float b[16];
+          cr[i].values(b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(r[i][j], r[i][j], sum);
-    }
-    const float rs = rsqrtf(row_sum(sum, part) / (float)K + a.eps);
+          for (int j = 0; j < 16; ++j) r[i][j] += b[j];
+        }
+      }
+      if (first + step < a.M) fetch(row + step);
+      float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int vec = threadIdx.x + i * blockDim.x;
-      finish(vec, live ? K - vec * 8 : 0, rs, r[i]);
+      for (int i = 0; i < NV; ++i) {
+        const int vec = threadIdx.x + i * blockDim.x;
+        if (res) store16<AL>(res_out + row * K + vec * 16, count(row, i), r[i]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum = fmaf(r[i][j], r[i][j], sum);
+      }
+      const float rs = rsqrtf(row_sum(sum, part[turn]) / (float)K + a.eps);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[i][j] = r[i][j] * rs * w[i][j];
+        emit16<OUT, AL>(a, (int)row, threadIdx.x + i * blockDim.x, count(row, i), r[i]);
+      }
     }
   } else {
-    const int steps = (K + 8 * (int)blockDim.x - 1) / (8 * (int)blockDim.x);
-    float r[8];
-    for (int i = 0; i < steps; ++i) {
-      const int vec = threadIdx.x + i * blockDim.x;
-      load(vec, live ? K - vec * 8 : 0, r);
+    int turn = 0;
+    for (long long first = (long long)blockIdx.x * blockDim.y; first < a.M; first += step, turn ^= 1) {
+      const long long row = first + threadIdx.y;
+      const bool live = row < a.M;
+      const auto load = [&](int vec, int n, float (&r)[16]) {
+        load16<AL>(x + row * a.ldx + vec * 16, n, r);
+        if (res) {
+          float b[16];
+          load16<AL>(res + row * K + vec * 16, n, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(r[j], r[j], sum);
-    }
-    const float rs = rsqrtf(row_sum(sum, part) / (float)K + a.eps);
-    for (int i = 0; i < steps; ++i) {
-      const int vec = threadIdx.x + i * blockDim.x;
-      const int n = live ? K - vec * 8 : 0;
-      load(vec, n, r);
-      if (res_out) store8<AL>(res_out + vec * 8, n, r);
-      finish(vec, n, rs, r);
+          for (int j = 0; j < 16; ++j) r[j] += b[j];
+        }
+      };
+      const int rounds = (K + 16 * (int)blockDim.x - 1) / (16 * (int)blockDim.x);
+      float r[16], sum = 0.f;
+      for (int i = 0; i < rounds; ++i) {
+        const int vec = threadIdx.x + i * blockDim.x;
+        load(vec, live ? K - vec * 16 : 0, r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum = fmaf(r[j], r[j], sum);
+      }
+      const float rs = rsqrtf(row_sum(sum, part[turn]) / (float)K + a.eps);
+      for (int i = 0; i < rounds; ++i) {
+        const int vec = threadIdx.x + i * blockDim.x;
+        const int n = live ? K - vec * 16 : 0;
+        load(vec, n, r);
+        if (res) store16<AL>(res_out + row * K + vec * 16, n, r);
+        float w[16];
+        if (a.w) {
+          load16_typed<AL>(a.w, a.w_type, vec * 16, n, w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = r[j] * rs * w[j];
+        emit16<OUT, AL>(a, (int)row, vec, n, r);
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
 // gated SiLU  y = g / (1 + e^-g) * u,  and (GATE = false) the plain copy that
-// the activation quantizer is.  One vector a thread; `chunks` CTAs a row.
+// the activation quantizer is.  A warp takes 32 vectors of a row at a time
+// (`parts` of them a row), the next ones' loads under way.
 // ---------------------------------------------------------------------------
 // FAST (outputs of 16 or 8 bits): the hardware's exponential and reciprocal.
 // Their error, about 2^-22 plus 2^-24 per unit of |g|, stays far below half a
@@ -365,23 +473,45 @@ __device__ __forceinline__ float silu(float g) {
   return g / (1.f + expf(-g));
 }
 
-template <typename T, bool GATE, int OUT, bool AL>
-__global__ void __launch_bounds__(256) rows_kernel(const RowArgs a, int chunks) {
+template <typename T, bool GATE, int OUT, int AL>
+__global__ void __launch_bounds__(256) rows_kernel(const RowArgs a, int parts) {
   pdl_launch_dependents();
   pdl_wait();
-  const int row = blockIdx.x / chunks;
-  const int vec = (blockIdx.x - row * chunks) * 256 + threadIdx.x;
-  const int n = a.K - vec * 8;
-  const T* x = static_cast<const T*>(a.x) + (long long)row * a.ldx;
-  float v[8];
-  load8<AL>(x + vec * 8, n, v);
-  if constexpr (GATE) {
-    float u[8];
-    load8<AL>(x + a.K + vec * 8, n, u);
+  const T* x = static_cast<const T*>(a.x);
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (blockDim.x >> 5), warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int dr = warps / parts, dp = warps - dr * parts;   // one step, in rows and parts
+  long long row = warp / parts;
+  int part = warp - (int)row * parts;
+  Raw16<AL, T> g, u;
+  const auto fetch = [&] {
+    if (row < a.M) {
+      const int at = (part * 32 + lane) * 16, n = a.K - at;
+      g.load(x + row * a.ldx + at, n);
+      if constexpr (GATE) u.load(x + row * a.ldx + a.K + at, n);
+    }
+  };
+  fetch();
+  while (row < a.M) {
+    float v[16];
+    g.values(v);
+    float w[16];
+    if constexpr (GATE) u.values(w);
+    const long long r = row;
+    const int vec = part * 32 + lane;
+    row += dr;
+    part += dp;
+    if (part >= parts) {
+      part -= parts;
+      ++row;
+    }
+    fetch();
+    if constexpr (GATE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = silu<OUT != OUT_FP32>(v[i]) * u[i];
+      for (int i = 0; i < 16; ++i) v[i] = silu<OUT != OUT_FP32>(v[i]) * w[i];
+    }
+    emit16<OUT, AL>(a, (int)r, vec, a.K - vec * 16, v);
   }
-  emit8<OUT, AL>(a, row, vec, n, v);
 }
 
 }  // namespace dq

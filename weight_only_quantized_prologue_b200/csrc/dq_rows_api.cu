@@ -16,9 +16,9 @@ bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p)
 
 size_t out_bytes(int out) { return out == OUT_FP32 ? 4 : out <= OUT_FP16 ? 2 : 1; }
 
-// Natural alignment of every buffer; *al: whether whole 16-byte vectors can
-// be moved (8-byte ones for codes).
-dqgemm_status check_rows(const RowArgs& a, int type, int out, int halves, bool* al) {
+// Natural alignment of every buffer; *al: how whole vectors of 16 elements can
+// be moved (see load16).
+dqgemm_status check_rows(const RowArgs& a, int type, int out, int halves, int* al) {
   if (type < ROW_BF16 || type > ROW_FP32 || out < OUT_BF16 || out > OUT_STATIC) return DQ_ERR_INVALID_ARG;
   if (!a.x || !a.out || a.M < 1 || a.K < 1 || a.K > (1 << 28) || a.ldx < (long long)halves * a.K)
     return DQ_ERR_INVALID_ARG;
@@ -28,10 +28,33 @@ dqgemm_status check_rows(const RowArgs& a, int type, int out, int halves, bool* 
   if (!aligned_to(a.x, tb) || !aligned_to(a.out, ob) || (out == OUT_BLOCK && !aligned_to(a.scales, 4)) ||
       (a.res && (!aligned_to(a.res, tb) || !aligned_to(a.res_out, tb))) || (a.w && !aligned_to(a.w, type_bytes(a.w_type))))
     return DQ_ERR_ALIGNMENT;
-  *al = a.K % 8 == 0 && aligned16(a.x) && (a.ldx * (long long)tb) % 16 == 0 && aligned_to(a.out, ob == 1 ? 8 : 16) &&
-        (!a.res || (aligned16(a.res) && aligned16(a.res_out))) && (!a.w || aligned16(a.w));
+  const auto fits = [&](int elems, size_t bytes) {
+    return a.K % elems == 0 && aligned_to(a.x, bytes) && (a.ldx * (long long)tb) % (long long)bytes == 0 &&
+           aligned_to(a.out, ob == 1 ? bytes / 2 : bytes) &&
+           (!a.res || (aligned_to(a.res, bytes) && aligned_to(a.res_out, bytes))) && (!a.w || aligned_to(a.w, bytes));
+  };
+  *al = fits(16, 32) ? 2 : fits(8, 16) ? 1 : 0;
   return DQ_OK;
 }
+
+// multiprocessors of the current device
+int sm_count() {
+  static int counts[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (counts[dev] == 0) {   // (every thread would write the same value)
+    int n = 0;
+    counts[dev] = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0 ? n : 148;
+  }
+  return counts[dev];
+}
+
+// threads a multiprocessor that a launch over many rows starts: each keeps the
+// loads of its next vectors in flight
+#ifndef ROW_THREADS
+#define ROW_THREADS 1024
+#endif
+constexpr int kRowThreads = ROW_THREADS;
 
 template <typename... KArgs, typename... Args>
 dqgemm_status launch_rows(void (*kern)(KArgs...), dim3 grid, dim3 block, void* stream, Args... args) {
@@ -47,42 +70,46 @@ dqgemm_status launch_rows(void (*kern)(KArgs...), dim3 grid, dim3 block, void* s
   return cuda_err(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...));
 }
 
-template <typename T, int OUT, bool AL>
+template <typename T, int OUT, int AL>
 dqgemm_status norm_launch(const RowArgs& a, void* stream) {
-  // threads a row: one vector each up to 512 of them (K = 4096), then 2 and 4
-  // vectors each; longer rows are read twice
-  const int vecs = (a.K + 7) / 8;
-  int tpr = 32;
-  while (tpr < 512 && tpr < vecs) tpr *= 2;
+  // threads a row: one vector each up to 512 of them (K = 8192), then two;
+  // rows past K = 16384 are read twice
+  const int vecs = (a.K + 15) / 16;
+  const int tpr = std::min(512, (vecs + 31) / 32 * 32);
   const int per = (vecs + tpr - 1) / tpr;
   const int rows = std::max(1, 128 / tpr);
   const dim3 block(tpr, rows);
-  const dim3 grid((unsigned)((a.M + rows - 1) / rows));
-  if (per <= 1) return launch_rows(rmsnorm_kernel<T, 1, OUT, AL>, grid, block, stream, a);
-  if (per <= 2) return launch_rows(rmsnorm_kernel<T, 2, OUT, AL>, grid, block, stream, a);
-  if (per <= 4) return launch_rows(rmsnorm_kernel<T, 4, OUT, AL>, grid, block, stream, a);
-  return launch_rows(rmsnorm_kernel<T, 0, OUT, AL>, grid, block, stream, a);
+  const int ctas = (int)std::min<long long>((a.M + (long long)rows - 1) / rows, (long long)sm_count() * (kRowThreads / (tpr * rows)));
+  if (per <= 1) return launch_rows(rmsnorm_kernel<T, 1, OUT, AL>, dim3(ctas), block, stream, a);
+  if (per <= 2) return launch_rows(rmsnorm_kernel<T, 2, OUT, AL>, dim3(ctas), block, stream, a);
+  return launch_rows(rmsnorm_kernel<T, 0, OUT, AL>, dim3(ctas), block, stream, a);
 }
 
-template <typename T, bool GATE, int OUT, bool AL>
+template <typename T, bool GATE, int OUT, int AL>
 dqgemm_status plain_launch(const RowArgs& a, void* stream) {
-  const int chunks = ((a.K + 7) / 8 + 255) / 256;
-  const long long ctas = (long long)chunks * a.M;
-  if (ctas > 0x7FFFFFFFll) return DQ_ERR_UNSUPPORTED;
-  return launch_rows(rows_kernel<T, GATE, OUT, AL>, dim3((unsigned)ctas), dim3(256), stream, a, chunks);
+  const int parts = (a.K + 511) / 512;
+  const long long items = (long long)parts * a.M;
+  // (few warps: one a CTA, so that they spread over the multiprocessors)
+  const int per = (int)std::max<long long>(1, std::min<long long>(8, items / sm_count()));
+  const int ctas = (int)std::min<long long>((items + per - 1) / per, (long long)sm_count() * (kRowThreads / (32 * per)));
+  return launch_rows(rows_kernel<T, GATE, OUT, AL>, dim3(ctas), dim3(32 * per), stream, a, parts);
 }
 
 // OP 0: rmsnorm, 1: gated SiLU, 2: plain (block-quantized output only)
 template <int OP, typename T, int OUT>
-dqgemm_status go(const RowArgs& a, bool al, void* stream) {
+dqgemm_status go(const RowArgs& a, int al, void* stream) {
   if constexpr (OP == 0)
-    return al ? norm_launch<T, OUT, true>(a, stream) : norm_launch<T, OUT, false>(a, stream);
+    return al == 2   ? norm_launch<T, OUT, 2>(a, stream)
+           : al == 1 ? norm_launch<T, OUT, 1>(a, stream)
+                     : norm_launch<T, OUT, 0>(a, stream);
   else
-    return al ? plain_launch<T, OP == 1, OUT, true>(a, stream) : plain_launch<T, OP == 1, OUT, false>(a, stream);
+    return al == 2   ? plain_launch<T, OP == 1, OUT, 2>(a, stream)
+           : al == 1 ? plain_launch<T, OP == 1, OUT, 1>(a, stream)
+                     : plain_launch<T, OP == 1, OUT, 0>(a, stream);
 }
 
 template <int OP, typename T>
-dqgemm_status go_out(const RowArgs& a, int out, bool al, void* stream) {
+dqgemm_status go_out(const RowArgs& a, int out, int al, void* stream) {
   if constexpr (OP == 2) {
     return go<OP, T, OUT_BLOCK>(a, al, stream);
   } else {
@@ -99,7 +126,7 @@ dqgemm_status go_out(const RowArgs& a, int out, bool al, void* stream) {
 template <int OP>
 dqgemm_status run_rows(RowArgs& a, int type, int out, float s_out, void* stream) {
   a.s_out = out == OUT_STATIC ? s_out : 1.f;
-  bool al = false;
+  int al = 0;
   const dqgemm_status st = check_rows(a, type, out, OP == 1 ? 2 : 1, &al);
   if (st != DQ_OK) return st;
   volatile float one = 1.f;

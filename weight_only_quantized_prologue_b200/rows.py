@@ -25,7 +25,6 @@ import torch
 from . import _native, _require
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # _native.ROW_TYPES, ROW_OUTS
-_QUANTS = {"fp8_block": 3, "fp8_static": 4}
 _one_device = None
 
 
@@ -52,48 +51,66 @@ def _rows(x, name, halves=1):
     if width % halves or width == 0:
         raise ValueError(f"{name} must hold {halves} halves of at least one column" if halves > 1
                          else f"{name} must have at least one column")
+    if x.is_contiguous():
+        return M, width // halves, width
     ld, inner = x.stride()
     if (inner != 1 and width != 1) or (M > 1 and ld < width):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return M, width // halves, ld if M > 1 else width
 
 
+def _new(x, M, K, dtype):
+    # (empty_strided: the cheapest of torch's allocating calls on the host)
+    return torch.empty_strided((M, K), (K, 1), dtype=dtype, device=x.device)
+
+
+def _given(t, name, M, K, dtype, x):
+    """A given [M, K] operand of x's device: checked the short way, and only a
+    misfit by _require, which names it."""
+    if not (t.dtype is dtype and t.dim() == 2 and t.shape[0] == M and t.shape[1] == K and t.is_contiguous()
+            and t.get_device() == x.get_device() and t.is_cuda):
+        _require(t, name, shape=(M, K), dtype=dtype, device=x.device)
+
+
 def _outputs(x, M, K, quant, s_out, out_dtype, out, scales):
     """(kind, s_out, out, scales) with what is not given allocated."""
-    dev = x.device
+    if quant == "fp8_block":
+        if out_dtype is not None:
+            raise ValueError("out_dtype goes with quant=None")
+        if s_out is not None:
+            raise ValueError("s_out goes with quant='fp8_static'")
+        if out is None:
+            out = _new(x, M, K, torch.uint8)
+        else:
+            _given(out, "out", M, K, torch.uint8, x)
+        kb = (K + 127) // 128
+        if scales is None:
+            scales = _new(x, M, kb, torch.float32)
+        else:
+            _given(scales, "scales", M, kb, torch.float32, x)
+        return 3, 1.0, out, scales
+    if scales is not None:
+        raise ValueError("scales go with quant='fp8_block'")
     if quant is None:
-        if scales is not None or s_out is not None:
-            raise ValueError("scales and s_out belong to quantized outputs (quant=...)")
+        if s_out is not None:
+            raise ValueError("s_out goes with quant='fp8_static'")
         dt = x.dtype if out_dtype is None else out_dtype
         if dt not in _TYPES:
             raise TypeError(f"out_dtype must be bfloat16, float16 or float32, got {dt}")
-        if out is None:
-            out = torch.empty((M, K), dtype=dt, device=dev)
-        else:
-            _require(out, "out", shape=(M, K), dtype=dt, device=dev)
-        return _TYPES[dt], 1.0, out, None
-    if quant not in _QUANTS:
-        raise ValueError(f"unknown quant {quant!r}; None, 'fp8_block' or 'fp8_static'")
-    if out_dtype is not None:
-        raise ValueError("out_dtype goes with quant=None")
-    if out is None:
-        out = torch.empty((M, K), dtype=torch.uint8, device=dev)
-    else:
-        _require(out, "out", shape=(M, K), dtype=torch.uint8, device=dev)
-    if quant == "fp8_static":
-        if scales is not None:
-            raise ValueError("scales go with quant='fp8_block'")
+        kind, s_out = _TYPES[dt], 1.0
+    elif quant == "fp8_static":
+        if out_dtype is not None:
+            raise ValueError("out_dtype goes with quant=None")
         if s_out is None or not (math.isfinite(s_out) and s_out > 0):
             raise ValueError("quant='fp8_static' needs a finite s_out > 0")
-        return 4, float(s_out), out, None
-    if s_out is not None:
-        raise ValueError("s_out goes with quant='fp8_static'")
-    shape = (M, (K + 127) // 128)
-    if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=dev)
+        dt, kind, s_out = torch.uint8, 4, float(s_out)
     else:
-        _require(scales, "scales", shape=shape, dtype=torch.float32, device=dev)
-    return 3, 1.0, out, scales
+        raise ValueError(f"unknown quant {quant!r}; None, 'fp8_block' or 'fp8_static'")
+    if out is None:
+        out = _new(x, M, K, dt)
+    else:
+        _given(out, "out", M, K, dt, x)
+    return kind, s_out, out, None
 
 
 def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out_dtype=None, out=None, scales=None,
@@ -108,33 +125,38 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out
     itself, or a contiguous x."""
     M, K, ld = _rows(x, "x")
     dev = x.get_device()
-    check_current(dev)
+    if _one_device is not True:
+        check_current(dev)
+    dt = x.dtype
+    wt = wp = rp = np = None
     if weight is not None:
-        if weight.dtype not in _TYPES:
+        wt = _TYPES.get(weight.dtype)
+        if wt is None:
             raise TypeError(f"weight must be bfloat16, float16 or float32, got {weight.dtype}")
-        _require(weight, "weight", shape=(K,), device=x.device)
+        if not (weight.dim() == 1 and weight.shape[0] == K and weight.is_contiguous() and weight.get_device() == dev):
+            _require(weight, "weight", shape=(K,), device=x.device)
+        wp = weight.data_ptr()
     if residual is not None:
-        _require(residual, "residual", shape=(M, K), dtype=x.dtype, device=x.device)
+        _given(residual, "residual", M, K, dt, x)
         if residual_out is None:
-            residual_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
-        else:
-            _require(residual_out, "residual_out", shape=(M, K), dtype=x.dtype, device=x.device)
+            residual_out = _new(x, M, K, dt)
+        elif residual_out is not residual:
+            _given(residual_out, "residual_out", M, K, dt, x)
+        rp, np = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    eps = float(eps)
-    if not (math.isfinite(eps) and eps >= 0):
+    if not 0 <= eps < math.inf:
         raise ValueError(f"eps must be finite and not negative, got {eps}")
     kind, s_out, out, scales = _outputs(x, M, K, quant, s_out, out_dtype, out, scales)
     if M:
-        _native._check(_native.lib().dqgemm_rmsnorm(
-            _TYPES[x.dtype], x.data_ptr(), ld, None if residual is None else residual.data_ptr(),
-            None if residual is None else residual_out.data_ptr(), 0 if weight is None else _TYPES[weight.dtype],
-            None if weight is None else weight.data_ptr(), eps, M, K, kind, s_out, out.data_ptr(),
-            None if scales is None else scales.data_ptr(), _native.device_stream(stream, dev)), "dqgemm_rmsnorm")
-    r = (out,) if scales is None else (out, scales)
-    if residual is not None:
-        r += (residual_out,)
-    return r if len(r) > 1 else out
+        st = _native.lib().dqgemm_rmsnorm(_TYPES[dt], x.data_ptr(), ld, rp, np, wt or 0, wp, eps, M, K, kind, s_out,
+                                          out.data_ptr(), None if scales is None else scales.data_ptr(),
+                                          _native.device_stream(stream, dev))
+        if st:
+            raise _native.DQError(st, "dqgemm_rmsnorm")
+    if residual is None:
+        return out if scales is None else (out, scales)
+    return (out, residual_out) if scales is None else (out, scales, residual_out)
 
 
 def silu_mul(x, quant=None, s_out=None, out_dtype=None, out=None, scales=None, stream=None):
@@ -143,7 +165,8 @@ def silu_mul(x, quant=None, s_out=None, out_dtype=None, out=None, scales=None, s
     outputs as for ``rmsnorm``."""
     M, K, ld = _rows(x, "x", 2)
     dev = x.get_device()
-    check_current(dev)
+    if _one_device is not True:
+        check_current(dev)
     kind, s_out, out, scales = _outputs(x, M, K, quant, s_out, out_dtype, out, scales)
     if M:
         _native._check(_native.lib().dqgemm_silu_mul(
@@ -157,7 +180,8 @@ def quantize_act_fp8_block(x, out=None, scales=None, stream=None):
     fp32 [M, ceil(K / 128)]).  Types and strides as for ``rmsnorm``."""
     M, K, ld = _rows(x, "x")
     dev = x.get_device()
-    check_current(dev)
+    if _one_device is not True:
+        check_current(dev)
     _, _, out, scales = _outputs(x, M, K, "fp8_block", None, None, out, scales)
     if M:
         _native._check(_native.lib().dqgemm_quantize_act_fp8_block(
