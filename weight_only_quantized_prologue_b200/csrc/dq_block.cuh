@@ -173,7 +173,28 @@ __device__ __forceinline__ bool mbar_try_wait3(uint64_t* a, uint32_t pa, uint64_
       : "memory");
   return ok != 0;
 }
-// the whole warp: every lane observes the phase itself
+// the whole warp on two barriers at once: every lane observes the phases itself
+__device__ __forceinline__ bool block_wait_warp2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, const WaitCtl ctl) {
+  uint64_t t0 = 0;
+  for (int i = ctl.timeout_ns < 1000u ? 63 : 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "and.pred p, p, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb)
+        : "memory");
+    if (__all_sync(0xFFFFFFFFu, ok != 0u)) return true;
+    if ((i & 63) == 63) {
+      if (t0 == 0) t0 = globaltimer_ns();
+      if (__any_sync(0xFFFFFFFFu, wait_give_up(ctl, t0))) return false;
+    }
+  }
+}
+// ... and on one
 __device__ __forceinline__ bool block_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtl ctl) {
   uint64_t t0 = 0;
   for (int i = ctl.timeout_ns < 1000u ? 63 : 0;; ++i) {
@@ -260,26 +281,28 @@ __device__ __forceinline__ void load_scales(const float* row, bool live, int b, 
 // of a block wait for its scales too (through full_x): nobody falls a whole
 // phase of a barrier behind, where a parity would be taken for the next.
 // ---------------------------------------------------------------------------
-template <int BN, bool XBF>
+template <int BN, bool GROUPED, bool XBF>
 struct SkinnyCfg {
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_BYTES = BN * 128;
   static constexpr int STAGE = W_BYTES + X_BYTES;          // both multiples of 1024
-  // two CTAs an SM up to 64 rows (also the next call's beside this one's),
-  // one at 128
-  static constexpr int ST = BN == 16 ? 5 : BN == 32 ? 5 : BN == 64 ? 4 : 6;
+  // Two CTAs an SM up to 32 rows (also the next call's beside this one's), one
+  // beyond.  Grouped: one with the whole ring, since 148 CTAs share out T
+  // tiles in ceil(T / 148) rounds and 296 in twice ceil(T / 296), which is
+  // never fewer.
+  static constexpr int CTAS = BN <= 32 && !GROUPED ? 2 : 1;
+  static constexpr int ST = BN <= 32 ? (CTAS == 2 ? 5 : 9) : BN == 64 ? 8 : 6;
   static constexpr int PB = 4;                             // partial buffers
   static constexpr int SR = ST + PB;                       // scale entries
   static constexpr int TMEM_COLS = PB * BN < 32 ? 32 : PB * BN;
   static constexpr int HALF = BN / 2;                      // columns per epilogue thread
   static constexpr int BAR_OFF = ST * STAGE;
-  static constexpr int BAR_BYTES = 384;
+  static constexpr int BAR_BYTES = 448;
   static constexpr int SC_OFF = BAR_OFF + BAR_BYTES;
   static constexpr int SC_BYTES = SR * BN * 4;
   static constexpr int TAB_OFF = SC_OFF + SC_BYTES;        // grouped: tile counts
   static constexpr int TAB_BYTES = (MAX_EXPERTS + 1) * 4;
   static constexpr int SMEM = TAB_OFF + TAB_BYTES + 1024;
-  static constexpr int CTAS = BN <= 64 ? 2 : 1;
   static constexpr int THREADS = XBF ? 512 : 384;
   static_assert(X_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(!XBF || BN == 16, "the quantizing warps keep up with a few rows only");
@@ -351,10 +374,10 @@ __device__ __forceinline__ void quantize_stage(const __nv_bfloat16* x, int K, in
 }
 
 template <int BN, bool GROUPED, bool XBF>
-__global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, SkinnyCfg<BN, XBF>::CTAS)
+__global__ void __launch_bounds__(SkinnyCfg<BN, GROUPED, XBF>::THREADS, SkinnyCfg<BN, GROUPED, XBF>::CTAS)
     block_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                         const BlockParams p) {
-  using C = SkinnyCfg<BN, XBF>;
+  using C = SkinnyCfg<BN, GROUPED, XBF>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full_w = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
@@ -556,7 +579,7 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, SkinnyCfg<BN, XBF
     const int qd = warp & 3, h = (warp - 4) >> 2;
     const int r = qd * 32 + lane;                       // channel within the tile
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
-    constexpr int LD = C::HALF < 16 ? C::HALF : 16;
+    constexpr int LD = C::HALF < 32 ? C::HALF : 32;
     int pb = 0, e = 0;
     uint32_t pph = 0, eph = 0;
     bool ok = true;
@@ -566,7 +589,7 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, SkinnyCfg<BN, XBF
 #pragma unroll
       for (int i = 0; i < C::HALF; ++i) acc[i] = 0.f;
       for (int b = b0; b < b1; ++b) {
-        if (!block_wait_warp(&sc_full[e], eph, ctl()) || !block_wait_warp(&acc_full[pb], pph, ctl())) { ok = false; break; }
+        if (!block_wait_warp2(&sc_full[e], eph, &acc_full[pb], pph, ctl())) { ok = false; break; }
         tc_fence_after();
         const float* f = scales + e * BN + h * C::HALF;
 #pragma unroll

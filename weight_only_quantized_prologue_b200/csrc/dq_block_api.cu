@@ -30,7 +30,7 @@ struct BlockPlan {
 template <int BN, bool G, bool X>
 cudaError_t skinny_attr() {
   cudaError_t e = cudaFuncSetAttribute(block_skinny_kernel<BN, G, X>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       SkinnyCfg<BN, X>::SMEM);
+                                       SkinnyCfg<BN, G, X>::SMEM);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(block_skinny_kernel<BN, G, X>, cudaFuncAttributePreferredSharedMemoryCarveout,
                              (int)cudaSharedmemCarveoutMaxShared);
@@ -57,15 +57,44 @@ cudaError_t set_attrs() {
   return e;
 }
 
-int ctas_per_sm(int bn) { return bn <= 64 ? 2 : 1; }
-
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// the largest power of two S <= 8, S <= kb, with T * S CTAs resident at once
-int pick_split(const dqgemm_s* h, long long T, int bn) {
-  const long long slots = (long long)h->num_sms * ctas_per_sm(bn);
+int force_split() {
+  static const int s = [] {
+    const char* e = std::getenv("DQGEMM_SPLIT");
+    return e ? std::atoi(e) : 0;
+  }();
+  return s;
+}
+
+// Whether a call on bf16 activations quantizes them in the product itself: up
+// to 8 rows (experts: 16, or 4 an expert on the mean), which the quantizing
+// warps handle within the weight's stream.  Beyond, quantizing them once ahead
+// is faster: 1 x 4096 x 14336 14.9 us either way, but 16 rows 20.5 against 15.3.
+bool quantizes(const dqgemm_s* h, int M, bool grouped) {
+  return grouped ? M <= 16 || M <= 4 * h->E : M <= 8;
+}
+
+// The split of K: the largest power of two S <= 8, S <= kb, with a CTA for each
+// of the T * S parts on an SM of its own (1 x 4096 x 4096, T = 32: S = 4 7.1 us,
+// S = 8 on half-shared SMs 7.6).  Tiles of up to 32 rows go to two CTAs an SM
+// where that still leaves each a long stream and half the SMs would have the
+// longest ones alone (1 x 14336 x 4096: S = 8 13.7 us, S = 4 14.6; but 1 x 4096
+// x 14336, T = 112: S = 2 14.1, S = 1 13.8), and where a call on bf16 quantizes
+// its few activations in each CTA, work that the split divides too (the same
+// call so: S = 2 15.3 us, S = 1 19.4; on codes as well, so that both add in one
+// order and give the same bits).
+int pick_split(const dqgemm_s* h, long long T, int bn, int M) {
   int s = 1;
-  while (s < 8 && 2 * s <= h->k_stages && T * 2 * s <= slots) s *= 2;
+  if (force_split() > 0) {
+    while (2 * s <= std::min({force_split(), 8, h->k_stages})) s *= 2;
+    return s;
+  }
+  const auto may_double = [&](long long slots) { return s < 8 && 2 * s <= h->k_stages && T * 2 * s <= slots; };
+  while (may_double(h->num_sms)) s *= 2;
+  if (bn <= 32 && may_double(2ll * h->num_sms) &&
+      (quantizes(h, M, false) || (h->k_stages / (2 * s) >= 14 && 2 * T <= h->num_sms)))
+    s *= 2;
   return s;
 }
 
@@ -74,7 +103,7 @@ BlockPlan dense_plan(const dqgemm_s* h, int M) {
   pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   if (M > 64) {
     const long long t1 = ceil_div(M, 128) * h->n_tiles, t2 = ceil_div(M, 256) * ceil_div(h->N, 256);
-    const int s = pick_split(h, t1, 128);
+    const int s = pick_split(h, t1, 128, M);
     const long long c1 = ceil_div(t1 * s, h->num_sms) * ceil_div(h->k_stages, s) * 520;
     const long long c2 = ceil_div(t2, h->num_sms / 2) * h->k_stages * 600;
     if (c2 <= c1) {
@@ -89,8 +118,8 @@ BlockPlan dense_plan(const dqgemm_s* h, int M) {
     pl.split = 1;
     pl.grid = 2 * (int)std::min<long long>(T, h->num_sms / 2);
   } else {
-    pl.split = pick_split(h, T, pl.bn);
-    pl.grid = (int)std::min<long long>(T * pl.split, pl.split > 1 ? T * pl.split : (long long)h->num_sms * ctas_per_sm(pl.bn));
+    pl.split = pick_split(h, T, pl.bn, M);
+    pl.grid = (int)(pl.split > 1 ? T * pl.split : std::min<long long>(T, (long long)h->num_sms * (pl.bn <= 32 ? 2 : 1)));
   }
   return pl;
 }
@@ -108,7 +137,7 @@ BlockPlan grouped_plan(const dqgemm_s* h, int M) {
   // at most one partial row tile per expert with rows
   const long long T = (M / pl.bn + std::min(h->E, M)) * (long long)pl.n_tiles;
   pl.grid = pl.pair ? 2 * (int)std::min<long long>(T, h->num_sms / 2)
-                    : (int)std::min<long long>(T, (long long)h->num_sms * ctas_per_sm(pl.bn));
+                    : (int)std::min<long long>(T, h->num_sms);
   return pl;
 }
 
@@ -167,7 +196,7 @@ cudaError_t launch(K kern, int grid, int threads, int smem, int cluster, const C
 template <int BN, bool G, bool X>
 cudaError_t launch_skinny(const BlockPlan& pl, const CUtensorMap& tw, const CUtensorMap& tx, const BlockParams& p,
                           cudaStream_t s) {
-  using C = SkinnyCfg<BN, X>;
+  using C = SkinnyCfg<BN, G, X>;
   return launch(block_skinny_kernel<BN, G, X>, pl.grid, C::THREADS, C::SMEM, pl.split, tw, tx, p, s);
 }
 
@@ -185,15 +214,7 @@ cudaError_t launch_plan(const BlockPlan& pl, const CUtensorMap& tw, const CUtens
   }
 }
 
-// Whether a call on bf16 activations quantizes them in the product itself: up
-// to 8 rows (experts: 16, or 4 an expert on the mean), which the quantizing
-// warps handle within the weight's stream.  Beyond, quantizing them once ahead
-// is faster: 1 x 4096 x 14336 14.9 us either way, but 16 rows 20.5 against 15.3.
-bool quantizes(const dqgemm_s* h, int M, bool grouped) {
-  return grouped ? M <= 16 || M <= 4 * h->E : M <= 8;
-}
-
-// Codes q and scales sx, or (where quantizes(plan)) bf16 x; arguments checked
+// Codes q and scales sx, or (where quantizes()) bf16 x; arguments checked
 // by the callers.
 dqgemm_status run_block(dqgemm_handle h, const BlockPlan& pl, const void* q, const float* sx, const void* x, int M,
                         const int* offsets, void* y, void* stream) {
@@ -338,16 +359,17 @@ void block_fill_plan(dqgemm_handle h, int M, dqgemm_plan* pl) {
   pl->k_stages = h->k_stages;
   pl->grid = b.grid;
   pl->max_segments = b.split;
+  const bool g = h->E > 1;
   pl->stages = pl->x_stages = b.pair ? PairCfg::ST
-                              : b.bn == 16 ? SkinnyCfg<16, true>::ST
-                              : b.bn == 32 ? SkinnyCfg<32, false>::ST
-                              : b.bn == 64 ? SkinnyCfg<64, false>::ST
-                                           : SkinnyCfg<128, false>::ST;
+                              : b.bn == 16 ? (g ? SkinnyCfg<16, true, true>::ST : SkinnyCfg<16, false, true>::ST)
+                              : b.bn == 32 ? (g ? SkinnyCfg<32, true, false>::ST : SkinnyCfg<32, false, false>::ST)
+                              : b.bn == 64 ? SkinnyCfg<64, false, false>::ST
+                                           : SkinnyCfg<128, false, false>::ST;
   pl->smem_bytes = b.pair ? PairCfg::SMEM
-                   : b.bn == 16 ? SkinnyCfg<16, true>::SMEM
-                   : b.bn == 32 ? SkinnyCfg<32, false>::SMEM
-                   : b.bn == 64 ? SkinnyCfg<64, false>::SMEM
-                                : SkinnyCfg<128, false>::SMEM;
+                   : b.bn == 16 ? (g ? SkinnyCfg<16, true, true>::SMEM : SkinnyCfg<16, false, true>::SMEM)
+                   : b.bn == 32 ? (g ? SkinnyCfg<32, true, false>::SMEM : SkinnyCfg<32, false, false>::SMEM)
+                   : b.bn == 64 ? SkinnyCfg<64, false, false>::SMEM
+                                : SkinnyCfg<128, false, false>::SMEM;
   pl->workspace_bytes = x_workspace(h, M, h->E > 1);
   pl->weight_bytes = h->weight_bytes;
   const long long T = (long long)pl->m_tiles * b.n_tiles;
