@@ -245,13 +245,13 @@ dqgemm_status dqgemm_run_experts_quantized(dqgemm_handle h, const void* q, const
                                            void* y, void* stream);
 
 /* A block-scaled layer (offsets NULL) or experts on bf16 x [M, K], with the
- * workspace in the caller's hands.  Few rows (M <= 8; with offsets M <= 16 or
- * M <= 4 E) are quantized in the product's own kernel and need none: one
+ * workspace in the caller's hands.  A layer's calls of up to 8 rows, and small
+ * ones of experts, quantize x in the product's own kernel and need none: one
  * launch.  Else x is quantized into `workspace` first: two launches, chained.
  * workspace: device, 16-byte aligned, at least dqgemm_plan.workspace_bytes of
- * dqgemm_get_plan(h, M) (an upper bound for every call of up to M rows is
- * M * (K + 4 * ceil(K/128)) + 256); DQ_ERR_INVALID_ARG if it is missing or
- * smaller.  Nobody else may use it before the call's kernels are done.  The
+ * dqgemm_get_plan(h, M) (0 where none is needed; an upper bound for every call
+ * of up to M rows is M * (K + 4 * ceil(K/128)) + 256); DQ_ERR_INVALID_ARG if
+ * it is missing or smaller.  Nobody else may use it before the call's kernels are done.  The
  * result is the same as from dqgemm_quantize_act_fp8_block and the call on
  * its codes, bit by bit. */
 dqgemm_status dqgemm_run_fp8_block(dqgemm_handle h, const void* x, int M, const int* offsets, void* y, void* workspace,

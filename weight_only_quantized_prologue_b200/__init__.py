@@ -340,8 +340,9 @@ class QuantizedExperts:
         self.device = packed.device
         self._dev = self.device.index
         self._check_current = torch.cuda.device_count() > 1
-        self._few_rows = max(16, 4 * E)           # as QuantizedLinear's
         self._h = dqgemm_create_experts(fmt, E, K, N, packed, scales, bias)
+        # as QuantizedLinear's, by the library's rule for these sizes
+        self._few_rows = next((m for m in range(16, 0, -1) if self.plan(m)["workspace_bytes"] == 0), 0)
 
     @classmethod
     def from_float(cls, fmt, W, bias=None):

@@ -578,7 +578,7 @@ dqgemm_status dqgemm_create(dqgemm_handle* out, dqgemm_format fmt_, int K, int N
   const int fmt = internal_fmt((int)fmt_);
   dqgemm_status st = check_shape(fmt, K, N);
   if (st != DQ_OK) return st;
-  if (fmt == FMT_FP8B) return block_create(out, 1, K, N, packed_w, scales, bias);
+  if (fmt == FMT_FP8B) return block_create(out, false, 1, K, N, packed_w, scales, bias);
   if (!packed_w || !scales) return DQ_ERR_INVALID_ARG;
   if (!aligned16(packed_w) || !aligned16(scales) || (bias && !aligned16(bias))) return DQ_ERR_ALIGNMENT;
   if (!is_device_ptr(packed_w) || !is_device_ptr(scales) || (bias && !is_device_ptr(bias)))
@@ -743,7 +743,7 @@ static dqgemm_status run_gemm(dqgemm_handle h, const void* x, bool xq, int M, vo
                               void* stream) {
   if (!h || !x || !y || M < 1) return DQ_ERR_INVALID_ARG;
   if (h->fmt == FMT_FP8B) {
-    if (xq || yq || h->E != 1) return DQ_ERR_UNSUPPORTED;
+    if (xq || yq || h->experts) return DQ_ERR_UNSUPPORTED;
     return block_run_x(h, x, M, y, stream);
   }
   if (is_w4a4(h->fmt)) {

@@ -67,12 +67,15 @@ int force_split() {
   return s;
 }
 
-// Whether a call on bf16 activations quantizes them in the product itself: up
-// to 8 rows (experts: 16, or 4 an expert on the mean), which the quantizing
-// warps handle within the weight's stream.  Beyond, quantizing them once ahead
-// is faster: 1 x 4096 x 14336 14.9 us either way, but 16 rows 20.5 against 15.3.
-bool quantizes(const dqgemm_s* h, int M, bool grouped) {
-  return grouped ? M <= 16 || M <= 4 * h->E : M <= 8;
+// Whether a call on bf16 activations quantizes them in the product itself, one
+// launch instead of two.  A layer: up to 8 rows, which the quantizing warps
+// handle within the weight's stream (1 x 4096 x 14336 15.3 us, on codes 14.2;
+// 16 rows 20.5 against 15.7 with the quantizer ahead).  Experts, whose CTAs go
+// through several tiles: 16 rows and at most 16 blocks a CTA (7 x 1024 x 768:
+// 6.2 us, on codes 5.0; but 64 x 4096 x 2048, 24 of 32 experts: 46 against 36).
+bool quantizes(const dqgemm_s* h, int M) {
+  if (!h->experts) return M <= 8;
+  return M <= 16 && h->k_stages * ceil_div((long long)std::min(h->E, M) * h->n_tiles, h->num_sms) <= 16;
 }
 
 // The split of K: the largest power of two S <= 8, S <= kb, with a CTA for each
@@ -93,7 +96,7 @@ int pick_split(const dqgemm_s* h, long long T, int bn, int M) {
   const auto may_double = [&](long long slots) { return s < 8 && 2 * s <= h->k_stages && T * 2 * s <= slots; };
   while (may_double(h->num_sms)) s *= 2;
   if (bn <= 32 && may_double(2ll * h->num_sms) &&
-      (quantizes(h, M, false) || (h->k_stages / (2 * s) >= 14 && 2 * T <= h->num_sms)))
+      (quantizes(h, M) || (h->k_stages / (2 * s) >= 14 && 2 * T <= h->num_sms)))
     s *= 2;
   return s;
 }
@@ -247,15 +250,15 @@ dqgemm_status run_block(dqgemm_handle h, const BlockPlan& pl, const void* q, con
   return cuda_err(offsets ? launch_plan<true>(pl, tw, x ? tw : tx, p, s) : launch_plan<false>(pl, tw, x ? tw : tx, p, s));
 }
 
-long long x_workspace(const dqgemm_s* h, int M, bool grouped) {
-  return quantizes(h, M, grouped) ? 0 : ((long long)M * h->K + 255) / 256 * 256 + (long long)M * h->k_stages * 4;
+long long x_workspace(const dqgemm_s* h, int M) {
+  return quantizes(h, M) ? 0 : ((long long)M * h->K + 255) / 256 * 256 + (long long)M * h->k_stages * 4;
 }
 
 // x bf16: in one launch where the product quantizes it itself, else quantized
 // into the workspace `ws` (codes, then scales) first
 dqgemm_status run_x(dqgemm_handle h, const void* x, int M, const int* offsets, void* y, void* ws, void* stream) {
   const BlockPlan pl = offsets ? grouped_plan(h, M) : dense_plan(h, M);
-  if (quantizes(h, M, offsets != nullptr)) return run_block(h, pl, nullptr, nullptr, x, M, offsets, y, stream);
+  if (quantizes(h, M)) return run_block(h, pl, nullptr, nullptr, x, M, offsets, y, stream);
   float* sx = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)M * h->K + 255) / 256 * 256);
   const dqgemm_status st = dqgemm_quantize_act_fp8_block(DQ_BF16, x, h->K, M, h->K, ws, sx, stream);
   return st == DQ_OK ? run_block(h, pl, ws, sx, nullptr, M, offsets, y, stream) : st;
@@ -265,7 +268,7 @@ dqgemm_status run_x(dqgemm_handle h, const void* x, int M, const int* offsets, v
 
 namespace dq {
 
-dqgemm_status block_create(dqgemm_handle* out, int E, int K, int N, const void* packed_w, const void* scales,
+dqgemm_status block_create(dqgemm_handle* out, bool experts, int E, int K, int N, const void* packed_w, const void* scales,
                            const void* bias) {
   // (out set to null and the shape checked by the callers)
   if (!packed_w || !scales) return DQ_ERR_INVALID_ARG;
@@ -278,6 +281,7 @@ dqgemm_status block_create(dqgemm_handle* out, int E, int K, int N, const void* 
   h->K = K;
   h->N = N;
   h->E = E;
+  h->experts = experts;
   h->k_stages = blocks(K);
   h->n_tiles = blocks(N);
   h->timeout_ns = timeout_ns();
@@ -324,7 +328,7 @@ dqgemm_status block_create(dqgemm_handle* out, int E, int K, int N, const void* 
 // dqgemm_run: the workspace, where one is needed, is the handle's
 dqgemm_status block_run_x(dqgemm_handle h, const void* x, int M, void* y, void* stream) {
   if (!aligned16(x) || !aligned16(y)) return DQ_ERR_ALIGNMENT;
-  const size_t total = (size_t)x_workspace(h, M, false);
+  const size_t total = (size_t)x_workspace(h, M);
   if (total > 0) {
     std::lock_guard<std::mutex> lock(h->maps_mu);
     if (h->ws_bytes < total) {
@@ -352,14 +356,14 @@ dqgemm_status block_dequantize(dqgemm_handle h, void* w_bf16, void* stream) {
 
 void block_fill_plan(dqgemm_handle h, int M, dqgemm_plan* pl) {
   std::memset(pl, 0, sizeof(*pl));
-  const BlockPlan b = h->E > 1 ? grouped_plan(h, M) : dense_plan(h, M);
+  const BlockPlan b = h->experts ? grouped_plan(h, M) : dense_plan(h, M);
   pl->bn = b.bn;
   pl->m_tiles = (int)ceil_div(M, b.bn);
   pl->n_tiles = b.n_tiles;
   pl->k_stages = h->k_stages;
   pl->grid = b.grid;
   pl->max_segments = b.split;
-  const bool g = h->E > 1;
+  const bool g = h->experts;
   pl->stages = pl->x_stages = b.pair ? PairCfg::ST
                               : b.bn == 16 ? (g ? SkinnyCfg<16, true, true>::ST : SkinnyCfg<16, false, true>::ST)
                               : b.bn == 32 ? (g ? SkinnyCfg<32, true, false>::ST : SkinnyCfg<32, false, false>::ST)
@@ -370,7 +374,7 @@ void block_fill_plan(dqgemm_handle h, int M, dqgemm_plan* pl) {
                    : b.bn == 32 ? (g ? SkinnyCfg<32, true, false>::SMEM : SkinnyCfg<32, false, false>::SMEM)
                    : b.bn == 64 ? SkinnyCfg<64, false, false>::SMEM
                                 : SkinnyCfg<128, false, false>::SMEM;
-  pl->workspace_bytes = x_workspace(h, M, h->E > 1);
+  pl->workspace_bytes = x_workspace(h, M);
   pl->weight_bytes = h->weight_bytes;
   const long long T = (long long)pl->m_tiles * b.n_tiles;
   const long long at_once = b.pair ? b.grid / 2 : b.grid;
@@ -413,13 +417,13 @@ dqgemm_status dqgemm_create_experts(dqgemm_handle* out, dqgemm_format fmt, int E
   if (E < 1 || K < 1 || N < 1 || (int)fmt < 0 || (int)fmt > (int)DQ_FP8_BLOCK128) return DQ_ERR_INVALID_ARG;
   if (fmt != DQ_FP8_BLOCK128 || E > MAX_EXPERTS) return DQ_ERR_UNSUPPORTED;
   if (K % 16) return DQ_ERR_INVALID_ARG;
-  return block_create(out, E, K, N, packed_w, scales, bias);
+  return block_create(out, true, E, K, N, packed_w, scales, bias);
 }
 
 dqgemm_status dqgemm_run_fp8_block_quantized(dqgemm_handle h, const void* q, const float* scales, int M, void* y,
                                              void* stream) {
   if (!h || !q || !scales || !y || M < 1) return DQ_ERR_INVALID_ARG;
-  if (h->fmt != FMT_FP8B || h->E != 1) return DQ_ERR_UNSUPPORTED;
+  if (h->fmt != FMT_FP8B || h->experts) return DQ_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(y) || reinterpret_cast<uintptr_t>(scales) % 4) return DQ_ERR_ALIGNMENT;
   return run_block(h, dense_plan(h, M), q, scales, nullptr, M, nullptr, y, stream);
 }
@@ -427,7 +431,7 @@ dqgemm_status dqgemm_run_fp8_block_quantized(dqgemm_handle h, const void* q, con
 dqgemm_status dqgemm_run_experts_quantized(dqgemm_handle h, const void* q, const float* scales, int M, const int* offsets,
                                            void* y, void* stream) {
   if (!h || !q || !scales || !offsets || !y || M < 1) return DQ_ERR_INVALID_ARG;
-  if (h->fmt != FMT_FP8B) return DQ_ERR_UNSUPPORTED;
+  if (h->fmt != FMT_FP8B || !h->experts) return DQ_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(y) || reinterpret_cast<uintptr_t>(scales) % 4 ||
       reinterpret_cast<uintptr_t>(offsets) % 4)
     return DQ_ERR_ALIGNMENT;
@@ -437,8 +441,8 @@ dqgemm_status dqgemm_run_experts_quantized(dqgemm_handle h, const void* q, const
 dqgemm_status dqgemm_run_fp8_block(dqgemm_handle h, const void* x, int M, const int* offsets, void* y, void* workspace,
                                    long long workspace_bytes, void* stream) {
   if (!h || !x || !y || M < 1) return DQ_ERR_INVALID_ARG;
-  if (h->fmt != FMT_FP8B || (!offsets && h->E != 1)) return DQ_ERR_UNSUPPORTED;
-  const long long need = x_workspace(h, M, offsets != nullptr);
+  if (h->fmt != FMT_FP8B || (offsets != nullptr) != h->experts) return DQ_ERR_UNSUPPORTED;
+  const long long need = x_workspace(h, M);
   if (need > 0 && (!workspace || workspace_bytes < need)) return DQ_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(y) || (need > 0 && !aligned16(workspace)) || reinterpret_cast<uintptr_t>(offsets) % 4)
     return DQ_ERR_ALIGNMENT;

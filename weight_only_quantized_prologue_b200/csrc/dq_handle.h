@@ -46,6 +46,7 @@ struct dqgemm_s {
   // block-scaled FP8 (fmt == FMT_FP8B): wchunks holds the canonical codes
   // [E * N, K], col_scale the block scales [E][N / 128][K / 128] (rounded up)
   int E = 1;
+  bool experts = false;             // made by dqgemm_create_experts: calls take offsets
   CUtensorMap wmap, wmap64;         // boxes of 128 k x 128 (64) rows of the codes
   std::mutex maps_mu;               // run entry points may be called from several threads
 };
@@ -58,7 +59,7 @@ constexpr int FMT_FP8B = 10;
 
 // block-scaled FP8 (dq_block_api.cu); arguments checked by the callers where
 // a comment says so
-dqgemm_status block_create(dqgemm_handle* out, int E, int K, int N, const void* packed_w, const void* scales,
+dqgemm_status block_create(dqgemm_handle* out, bool experts, int E, int K, int N, const void* packed_w, const void* scales,
                            const void* bias);
 dqgemm_status block_run_x(dqgemm_handle h, const void* x, int M, void* y, void* stream);
 dqgemm_status block_dequantize(dqgemm_handle h, void* w_bf16, void* stream);
