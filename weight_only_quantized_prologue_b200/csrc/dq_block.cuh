@@ -355,11 +355,10 @@ __device__ __forceinline__ void quantize_stage(const __nv_bfloat16* x, int K, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + 2 * i + half;   // (below the tile's 16: the rows that fill the last eight hold zeros)
-      float v[8];
-      unpack2(u[i].x, v[0], v[1], __nv_bfloat16());
-      unpack2(u[i].y, v[2], v[3], __nv_bfloat16());
-      unpack2(u[i].z, v[4], v[5], __nv_bfloat16());
-      unpack2(u[i].w, v[6], v[7], __nv_bfloat16());
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      F2 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
       uint2 c;
       if (fast) {
         c = codes8_fast(v, bs[i].s, bs[i].r);

@@ -17,6 +17,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "dq_common.cuh"
 
 namespace dq {
@@ -56,12 +58,49 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (sizeof(T) == 2) {
-    const T u = from_f32<T>(a), v = from_f32<T>(b);
-    return (uint32_t)*reinterpret_cast<const uint16_t*>(&u) | ((uint32_t)*reinterpret_cast<const uint16_t*>(&v) << 16);
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    return 0u;
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
+}
+
+// Two fp32 values side by side: one instruction works on both.  The kernels
+// hold their 16 elements as 8 such pairs.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float lo(F2 x) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+  return a;
+}
+__device__ __forceinline__ float hi(F2 x) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+  return b;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 
 __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, __nv_bfloat16) {
@@ -115,19 +154,19 @@ struct Raw16 {
       }
     }
   }
-  __device__ __forceinline__ void values(float (&v)[16]) const {
-    if constexpr (sizeof(T) == 4) {
+  __device__ __forceinline__ void values(F2 (&v)[8]) const {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
-    } else if constexpr (AL == 0) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint16_t h = (uint16_t)w[i];
-        v[i] = to_f32(*reinterpret_cast<const T*>(&h));
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      if constexpr (sizeof(T) == 4) {
+        a = __uint_as_float(w[2 * i]);
+        b = __uint_as_float(w[2 * i + 1]);
+      } else if constexpr (AL == 0) {
+        unpack2(w[2 * i] | (w[2 * i + 1] << 16), a, b, T());
+      } else {
+        unpack2(w[i], a, b, T());
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) unpack2(w[i], v[2 * i], v[2 * i + 1], T());
+      v[i] = f2(a, b);
     }
   }
   static __device__ __forceinline__ uint32_t bits(T v) {
@@ -137,25 +176,29 @@ struct Raw16 {
 };
 
 template <int AL, typename T>
-__device__ __forceinline__ void load16(const T* p, int n, float (&v)[16]) {
+__device__ __forceinline__ void load16(const T* p, int n, F2 (&v)[8]) {
   Raw16<AL, T> raw;
   raw.load(p, n);
   raw.values(v);
 }
 
 template <int AL, typename T>
-__device__ __forceinline__ void store16(T* p, int n, const float (&v)[16]) {
+__device__ __forceinline__ void store16(T* p, int n, const F2 (&v)[8]) {
   if constexpr (AL == 0) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i < n) p[i] = from_f32<T>(v[i]);
+      if (i < n) p[i] = from_f32<T>(i & 1 ? hi(v[i / 2]) : lo(v[i / 2]));
   } else {
     constexpr int WORDS = 4 * sizeof(T);
     uint32_t w[WORDS];
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      if constexpr (sizeof(T) == 2) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
-      else w[i] = __float_as_uint(v[i]);
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        w[i] = pack2<T>(lo(v[i]), hi(v[i]));
+      } else {
+        w[2 * i] = __float_as_uint(lo(v[i]));
+        w[2 * i + 1] = __float_as_uint(hi(v[i]));
+      }
     }
     if constexpr (AL == 2) {
       if (n > 0) {
@@ -171,7 +214,7 @@ __device__ __forceinline__ void store16(T* p, int n, const float (&v)[16]) {
 }
 
 template <int AL>
-__device__ __forceinline__ void load16_typed(const void* p, int type, long long at, int n, float (&v)[16]) {
+__device__ __forceinline__ void load16_typed(const void* p, int type, long long at, int n, F2 (&v)[8]) {
   if (type == ROW_BF16)
     load16<AL>(static_cast<const __nv_bfloat16*>(p) + at, n, v);
   else if (type == ROW_FP16)
@@ -216,34 +259,34 @@ __device__ __forceinline__ BlockScale block_scale_of(uint32_t amax_bits) {
   return b;
 }
 
-// f32(v / s), correctly rounded where the e4m3 code depends on it, without
-// the range test of e4m3_quotient: for r = f32(1 / s) normal and |v / s| not
-// above 2^9, the correction leaves every quotient below 2^-12 there (where
-// each code is 0) and cannot overflow.  The remainder is taken negated, so
-// that a zero keeps its sign through both steps.
-__device__ __forceinline__ float block_quotient(float v, float s, float r) {
-  const float q0 = __fmul_rn(v, r);
-  return __fmaf_rn(-__fmaf_rn(q0, s, -v), r, q0);
-}
-
-// The 8 codes of v under the scale s: e4m3(f32(v / s)), 0 where s is 0; for
-// blocks whose scale is `fast` ...
-__device__ __forceinline__ uint2 codes8_fast(const float* v, float s, float r) {
-  const uint32_t lo = e4m3x2(block_quotient(v[0], s, r), block_quotient(v[1], s, r)) |
-                      (e4m3x2(block_quotient(v[2], s, r), block_quotient(v[3], s, r)) << 16);
-  const uint32_t hi = e4m3x2(block_quotient(v[4], s, r), block_quotient(v[5], s, r)) |
-                      (e4m3x2(block_quotient(v[6], s, r), block_quotient(v[7], s, r)) << 16);
-  return s == 0.f ? make_uint2(0u, 0u) : make_uint2(lo, hi);
+// The 8 codes of 4 pairs under the scale s: e4m3(f32(v / s)), 0 where s is 0;
+// for blocks whose scale is `fast` ...
+// The quotient, correctly rounded where the code depends on it, without the
+// range test of e4m3_quotient: for r normal and |v / s| not above 2^9 the
+// correction leaves every quotient below 2^-12 there (where each code is 0) and
+// cannot overflow.  It is taken of -v, whose steps need no negation:
+//   q = -v r,  e = q s + v  (= q s - (-v)),  q - e r;
+// the codes' signs are flipped at the end, and a zero keeps its own.
+__device__ __forceinline__ uint2 codes8_fast(const F2* v, float s, float r) {
+  const F2 s2 = f2(s, s), nr = f2(-r, -r);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const F2 q = mul2(v[i], nr);
+    const F2 t = fma2(fma2(q, s2, v[i]), nr, q);
+    c[i] = e4m3x2(lo(t), hi(t));
+  }
+  return s == 0.f ? make_uint2(0u, 0u) : make_uint2((c[0] | (c[1] << 16)) ^ 0x80808080u, (c[2] | (c[3] << 16)) ^ 0x80808080u);
 }
 // ... and for any scale, by the division (a NaN makes every code of its block
 // NaN; in a block with an infinity the finite elements' codes are 0)
-__device__ __forceinline__ uint2 codes8_any(const float* v, float s) {
+__device__ __forceinline__ uint2 codes8_any(const F2* v, float s) {
   uint32_t w[2] = {0u, 0u};
   if (s != 0.f) {
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
-      const float a = h ? v[4] : v[0], b = h ? v[5] : v[1], c = h ? v[6] : v[2], d = h ? v[7] : v[3];
-      const uint32_t x = e4m3x2(__fdiv_rn(a, s), __fdiv_rn(b, s)) | (e4m3x2(__fdiv_rn(c, s), __fdiv_rn(d, s)) << 16);
+      const F2 a = h ? v[2] : v[0], b = h ? v[3] : v[1];
+      const uint32_t x = e4m3x2(__fdiv_rn(lo(a), s), __fdiv_rn(hi(a), s)) | (e4m3x2(__fdiv_rn(lo(b), s), __fdiv_rn(hi(b), s)) << 16);
       if (h) w[1] = x;
       else w[0] = x;
     }
@@ -260,23 +303,28 @@ __device__ __forceinline__ float amax2(float a, float b) {
 
 // Scale and codes of a warp's four blocks, 8 lanes each (the whole warp calls
 // this).  A NaN makes the maximum and so the scale NaN.
-__device__ __forceinline__ uint4 quantize_block(const float (&v)[16], float* s) {
-  float a = amax2(amax2(amax2(amax2(v[0], v[1]), amax2(v[2], v[3])), amax2(amax2(v[4], v[5]), amax2(v[6], v[7]))),
-                  amax2(amax2(amax2(v[8], v[9]), amax2(v[10], v[11])), amax2(amax2(v[12], v[13]), amax2(v[14], v[15]))));
+__device__ __forceinline__ uint4 quantize_block(const F2 (&v)[8], float* s) {
+  float a = amax2(lo(v[0]), hi(v[0])), b2 = amax2(lo(v[1]), hi(v[1]));
+#pragma unroll
+  for (int i = 2; i < 8; i += 2) {
+    a = amax2(a, amax2(lo(v[i]), hi(v[i])));
+    b2 = amax2(b2, amax2(lo(v[i + 1]), hi(v[i + 1])));
+  }
+  a = amax2(a, b2);
 #pragma unroll
   for (int o = 4; o; o >>= 1) a = amax2(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
   const BlockScale b = block_scale_of(__float_as_uint(a));
-  uint2 lo, hi;
+  uint2 c, d;
   if (__all_sync(0xFFFFFFFFu, b.fast)) {
     *s = b.s;
-    lo = codes8_fast(v, b.s, b.r);
-    hi = codes8_fast(v + 8, b.s, b.r);
+    c = codes8_fast(v, b.s, b.r);
+    d = codes8_fast(v + 4, b.s, b.r);
   } else {
     *s = __fdiv_rn(a, 448.f);
-    lo = codes8_any(v, *s);
-    hi = codes8_any(v + 8, *s);
+    c = codes8_any(v, *s);
+    d = codes8_any(v + 4, *s);
   }
-  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  return make_uint4(c.x, c.y, d.x, d.y);
 }
 
 template <int AL>
@@ -298,7 +346,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, uint4 c) {
 // The whole warp calls this, its lanes holding consecutive vectors from a
 // multiple of 32 on.
 template <int OUT, int AL>
-__device__ __forceinline__ void emit16(const RowArgs& a, int row, int vec, int n, const float (&v)[16]) {
+__device__ __forceinline__ void emit16(const RowArgs& a, int row, int vec, int n, const F2 (&v)[8]) {
   const long long at = (long long)row * a.K + vec * 16;
   if constexpr (OUT == OUT_BLOCK) {
     float s;
@@ -313,7 +361,8 @@ __device__ __forceinline__ void emit16(const RowArgs& a, int row, int vec, int n
     for (int h = 0; h < 4; ++h) {
       w[h] = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[h] |= (uint32_t)act_code_r(v[4 * h + i], a.s_out, a.r_out) << (8 * i);
+      for (int i = 0; i < 4; ++i)
+        w[h] |= (uint32_t)act_code_r(i & 1 ? hi(v[2 * h + i / 2]) : lo(v[2 * h + i / 2]), a.s_out, a.r_out) << (8 * i);
     }
     store_codes<AL>(static_cast<uint8_t*>(a.out) + at, n, make_uint4(w[0], w[1], w[2], w[3]));
   } else if constexpr (OUT == OUT_BF16) {
@@ -374,7 +423,7 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const RowArgs a) {
     };
     long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     fetch(row);
-    float w[NV][16];
+    F2 w[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int vec = threadIdx.x + i * blockDim.x;
@@ -382,37 +431,37 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const RowArgs a) {
         load16_typed<AL>(a.w, a.w_type, vec * 16, K - vec * 16, w[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) w[i][j] = 1.f;
+        for (int j = 0; j < 8; ++j) w[i][j] = f2(1.f, 1.f);
       }
     }
     int turn = 0;
     // (the bound is of the CTA's first row: its threads meet in row_sum)
     for (long long first = (long long)blockIdx.x * blockDim.y; first < a.M; first += step, row += step, turn ^= 1) {
-      float r[NV][16];
+      F2 r[NV][8];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         cx[i].values(r[i]);
         if (res) {
-          float b[16];
+          F2 b[8];
           cr[i].values(b);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) r[i][j] += b[j];
+          for (int j = 0; j < 8; ++j) r[i][j] = add2(r[i][j], b[j]);
         }
       }
       if (first + step < a.M) fetch(row + step);
-      float sum = 0.f;
+      F2 sum = f2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int vec = threadIdx.x + i * blockDim.x;
         if (res) store16<AL>(res_out + row * K + vec * 16, count(row, i), r[i]);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum = fmaf(r[i][j], r[i][j], sum);
+        for (int j = 0; j < 8; ++j) sum = fma2(r[i][j], r[i][j], sum);
       }
-      const float rs = rsqrtf(row_sum(sum, part[turn]) / (float)K + a.eps);
+      const float rs = rsqrtf(row_sum(lo(sum) + hi(sum), part[turn]) / (float)K + a.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[i][j] = r[i][j] * rs * w[i][j];
+        for (int j = 0; j < 8; ++j) r[i][j] = mul2(mul2(r[i][j], f2(rs, rs)), w[i][j]);
         emit16<OUT, AL>(a, (int)row, threadIdx.x + i * blockDim.x, count(row, i), r[i]);
       }
     }
@@ -421,38 +470,38 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const RowArgs a) {
     for (long long first = (long long)blockIdx.x * blockDim.y; first < a.M; first += step, turn ^= 1) {
       const long long row = first + threadIdx.y;
       const bool live = row < a.M;
-      const auto load = [&](int vec, int n, float (&r)[16]) {
+      const auto load = [&](int vec, int n, F2 (&r)[8]) {
         load16<AL>(x + row * a.ldx + vec * 16, n, r);
         if (res) {
-          float b[16];
+          F2 b[8];
           load16<AL>(res + row * K + vec * 16, n, b);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) r[j] += b[j];
+          for (int j = 0; j < 8; ++j) r[j] = add2(r[j], b[j]);
         }
       };
       const int rounds = (K + 16 * (int)blockDim.x - 1) / (16 * (int)blockDim.x);
-      float r[16], sum = 0.f;
+      F2 r[8], sum = f2(0.f, 0.f);
       for (int i = 0; i < rounds; ++i) {
         const int vec = threadIdx.x + i * blockDim.x;
         load(vec, live ? K - vec * 16 : 0, r);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum = fmaf(r[j], r[j], sum);
+        for (int j = 0; j < 8; ++j) sum = fma2(r[j], r[j], sum);
       }
-      const float rs = rsqrtf(row_sum(sum, part[turn]) / (float)K + a.eps);
+      const float rs = rsqrtf(row_sum(lo(sum) + hi(sum), part[turn]) / (float)K + a.eps);
       for (int i = 0; i < rounds; ++i) {
         const int vec = threadIdx.x + i * blockDim.x;
         const int n = live ? K - vec * 16 : 0;
         load(vec, n, r);
         if (res) store16<AL>(res_out + row * K + vec * 16, n, r);
-        float w[16];
+        F2 w[8];
         if (a.w) {
           load16_typed<AL>(a.w, a.w_type, vec * 16, n, w);
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) w[j] = 1.f;
+          for (int j = 0; j < 8; ++j) w[j] = f2(1.f, 1.f);
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = r[j] * rs * w[j];
+        for (int j = 0; j < 8; ++j) r[j] = mul2(mul2(r[j], f2(rs, rs)), w[j]);
         emit16<OUT, AL>(a, (int)row, vec, n, r);
       }
     }
@@ -468,9 +517,19 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const RowArgs a) {
 // Their error, about 2^-22 plus 2^-24 per unit of |g|, stays far below half a
 // step of the output wherever the result is not itself vanishing.
 template <bool FAST>
-__device__ __forceinline__ float silu(float g) {
-  if constexpr (FAST) return __fdividef(g, 1.f + __expf(-g));
-  return g / (1.f + expf(-g));
+__device__ __forceinline__ F2 silu_mul2(F2 g, F2 u) {
+  if constexpr (FAST) {
+    const F2 t = mul2(g, f2(-1.44269504f, -1.44269504f));   // log2 e
+    float e0, e1, r0, r1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(lo(t)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(hi(t)));
+    const F2 d = add2(f2(e0, e1), f2(1.f, 1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(lo(d)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(hi(d)));
+    return mul2(mul2(g, f2(r0, r1)), u);
+  } else {
+    return f2(lo(g) / (1.f + expf(-lo(g))) * lo(u), hi(g) / (1.f + expf(-hi(g))) * hi(u));
+  }
 }
 
 template <typename T, bool GATE, int OUT, int AL>
@@ -493,9 +552,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowArgs a, int parts) {
   };
   fetch();
   while (row < a.M) {
-    float v[16];
+    F2 v[8], w[8];
     g.values(v);
-    float w[16];
     if constexpr (GATE) u.values(w);
     const long long r = row;
     const int vec = part * 32 + lane;
@@ -508,7 +566,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowArgs a, int parts) {
     fetch();
     if constexpr (GATE) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = silu<OUT != OUT_FP32>(v[i]) * w[i];
+      for (int i = 0; i < 8; ++i) v[i] = silu_mul2<OUT != OUT_FP32>(v[i], w[i]);
     }
     emit16<OUT, AL>(a, (int)r, vec, a.K - vec * 16, v);
   }
