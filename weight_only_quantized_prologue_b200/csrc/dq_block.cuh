@@ -252,9 +252,16 @@ __device__ __forceinline__ void tmem_wait_regs(float (&v)[N]) {
   }
 }
 
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+// distributed shared memory: cluster CTA `rank`'s copy of a local address
+__device__ __forceinline__ float4 ld_dsmem_f4(uint32_t local, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(local), "r"(rank)
+      : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
@@ -272,7 +279,7 @@ __device__ __forceinline__ void load_scales(const float* row, bool live, int b, 
 // ---------------------------------------------------------------------------
 // skinny: 128 channels x BN rows per CTA
 // warps: 0 weight copies, 1 MMA, 2 activation copies, 3 scales, 4..11
-// epilogue; with bf16 activations (XBF) 12..15 quantize them instead of 2 and 3
+// epilogue; with bf16 activations (XBF) 12..19 quantize them instead of 2 and 3
 //
 // The combined scales sx * sw of each block of K go through a ring of their
 // own, [SR][BN].  It needs no barrier against reuse: who writes entry i + SR
@@ -281,17 +288,16 @@ __device__ __forceinline__ void load_scales(const float* row, bool live, int b, 
 // of a block wait for its scales too (through full_x): nobody falls a whole
 // phase of a barrier behind, where a parity would be taken for the next.
 // ---------------------------------------------------------------------------
-template <int BN, bool GROUPED, bool XBF>
+template <int BN, bool XBF>
 struct SkinnyCfg {
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_BYTES = BN * 128;
   static constexpr int STAGE = W_BYTES + X_BYTES;          // both multiples of 1024
-  // Two CTAs an SM up to 32 rows (also the next call's beside this one's), one
-  // beyond.  Grouped: one with the whole ring, since 148 CTAs share out T
-  // tiles in ceil(T / 148) rounds and 296 in twice ceil(T / 296), which is
-  // never fewer.
-  static constexpr int CTAS = BN <= 32 && !GROUPED ? 2 : 1;
-  static constexpr int ST = BN <= 32 ? (CTAS == 2 ? 5 : 9) : BN == 64 ? 8 : 6;
+  // One CTA an SM with the whole ring: 144 KB of weights in flight.  (Two an SM
+  // with five stages each: 1 x 4096 x 14336 13.7 us against 11.9, 32 rows 14.7
+  // against 12.1; and of grouped tiles T, 148 CTAs take ceil(T / 148) rounds,
+  // 296 twice ceil(T / 296), never fewer.)
+  static constexpr int ST = BN <= 32 ? 9 : BN == 64 ? 8 : 6;
   static constexpr int PB = 4;                             // partial buffers
   static constexpr int SR = ST + PB;                       // scale entries
   static constexpr int TMEM_COLS = PB * BN < 32 ? 32 : PB * BN;
@@ -303,29 +309,37 @@ struct SkinnyCfg {
   static constexpr int TAB_OFF = SC_OFF + SC_BYTES;        // grouped: tile counts
   static constexpr int TAB_BYTES = (MAX_EXPERTS + 1) * 4;
   static constexpr int SMEM = TAB_OFF + TAB_BYTES + 1024;
-  static constexpr int THREADS = XBF ? 512 : 384;
+  // quantizing warps (1 x 4096 x 14336: 8 of them 13.5 us, 4 14.4, codes 11.9)
+  static constexpr int QW = 8;
+  static constexpr int THREADS = 384 + (XBF ? 32 * QW : 0);
   static_assert(X_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(!XBF || BN == 16, "the quantizing warps keep up with a few rows only");
   static_assert(BN * 128 * 4 <= ST * STAGE, "the reduction reuses the ring");
-  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
-  static_assert(CTAS * TMEM_COLS <= 512, "tensor memory");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(TMEM_COLS <= 512, "tensor memory");
 };
 
 // One block of K of a tile's rows: 16 lanes a row, 8 elements a lane, two rows
 // an instruction.  Codes into the tensor core's swizzled rows, combined scales
 // into `sc`.  The same arithmetic as the row quantizer's.  Rows past m_end are
-// left out: what their columns hold is not stored.
-__device__ __forceinline__ void quantize_stage(const __nv_bfloat16* x, int K, int m0, int rows, int b, float sw, uint8_t* xs,
-                                               float* sc, int lane) {
+// left out: what their columns hold is not stored.  The first eight rows come
+// in `first`, fetched by load_rows8 while the warp's last block was quantized.
+__device__ __forceinline__ void load_rows8(const __nv_bfloat16* x, int K, int m0, int r0, int rows, int b, int lane,
+                                           uint4 (&u)[4]) {
   const int k = b * 128 + (lane & 15) * 8, half = lane >> 4;
   const __nv_bfloat16* src = x + (size_t)(m0 + half) * K + k;
-  for (int r0 = 0; r0 < rows; r0 += 8) {
-    // four row pairs at once: loads, maxima and quotients of one overlap the others'
-    uint4 u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      u[i] = r0 + 2 * i + half < rows && k < K ? *reinterpret_cast<const uint4*>(src + (size_t)(r0 + 2 * i) * K)
-                                               : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < 4; ++i)
+    u[i] = r0 + 2 * i + half < rows && k < K ? *reinterpret_cast<const uint4*>(src + (size_t)(r0 + 2 * i) * K)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ void quantize_stage(const uint4 (&first)[4], const __nv_bfloat16* x, int K, int m0, int rows, int b,
+                                               float sw, uint8_t* xs, float* sc, int lane) {
+  const int half = lane >> 4;
+  uint4 u[4] = {first[0], first[1], first[2], first[3]};
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    // four row pairs at once: maxima and quotients of one overlap the others'
+    if (r0 > 0) load_rows8(x, K, m0, r0, rows, b, lane, u);
     // the maxima as bf16 bits, two pairs of rows in a word
     uint32_t m[4];
 #pragma unroll
@@ -373,10 +387,10 @@ __device__ __forceinline__ void quantize_stage(const __nv_bfloat16* x, int K, in
 }
 
 template <int BN, bool GROUPED, bool XBF>
-__global__ void __launch_bounds__(SkinnyCfg<BN, GROUPED, XBF>::THREADS, SkinnyCfg<BN, GROUPED, XBF>::CTAS)
+__global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
     block_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                         const BlockParams p) {
-  using C = SkinnyCfg<BN, GROUPED, XBF>;
+  using C = SkinnyCfg<BN, XBF>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full_w = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
@@ -521,7 +535,7 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, GROUPED, XBF>::THREADS, SkinnyCf
       }
     }
   } else if (XBF && warp >= 12) {
-    // ------------------------------------------------------------ quantizer: warp w takes every fourth block
+    // ------------------------------------------------------------ quantizer: QW warps take the blocks in turn
     if constexpr (!GROUPED) pdl_wait();
     const int w = warp - 12;
     int it = 0;
@@ -530,11 +544,26 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, GROUPED, XBF>::THREADS, SkinnyCf
       const BlockTile tl = block_tile<BN, 128, GROUPED>(p, start, t);
       const float* sw = p.sw + ((size_t)tl.e * p.nb + (tl.n0 >> 7)) * p.kb;
       const int rows = min(BN, tl.m_end - tl.m0);
+      uint4 u[4], next[4];
+      float su = 0.f, snext = 0.f;
+      bool have = false;
       for (int b = b0; b < b1; ++b, ++it) {
-        if ((it & 3) != w) continue;
+        if (it % C::QW != w) continue;
+        if (!have) {
+          load_rows8(p.x, p.K, tl.m0, 0, rows, b, lane, next);
+          snext = sw[b];
+          have = true;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = next[i];
+        su = snext;
+        if (b + C::QW < b1) {
+          load_rows8(p.x, p.K, tl.m0, 0, rows, b + C::QW, lane, next);
+          snext = sw[b + C::QW];
+        }
         const int s = it % C::ST, e = it % C::SR;
         if (it >= C::ST && !block_wait_warp(&empty[s], (uint32_t)(it / C::ST + 1) & 1u, ctl())) { ok = false; break; }
-        quantize_stage(p.x, p.K, tl.m0, rows, b, sw[b], smem + s * C::STAGE + C::W_BYTES, scales + e * BN, lane);
+        quantize_stage(u, p.x, p.K, tl.m0, rows, b, su, smem + s * C::STAGE + C::W_BYTES, scales + e * BN, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -645,14 +674,32 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, GROUPED, XBF>::THREADS, SkinnyCf
       bool good = true;
       for (int q = 0; q < S; ++q) good = good && ld_dsmem_u32(dsmem_addr(const_cast<uint32_t*>(bad), q)) == 0u;
       if (good) {
-        for (int i = threadIdx.x - 128; i < cols * 128; i += 256) {
-          const int c = rank * cols + (i >> 7), n = tl.n0 + (i & 127), m = tl.m0 + c;
-          const float* cell = reinterpret_cast<const float*>(smem) + c * 128 + (i & 127);
-          float v = 0.f;
-          for (int q = 0; q < S; ++q) v += ld_dsmem_f32(dsmem_addr(cell, q));
-          if (n < p.N && m < tl.m_end) {
-            if (p.bias) v += __bfloat162float(p.bias[n]);
-            p.y[(size_t)m * p.N + n] = __float2bfloat16_rn(v);
+        // four channels of a column at a time, every rank's partials on their
+        // way before the first is added (one by one 128 x 4096 x 4096 took
+        // 14.1 us)
+        const uint32_t base = smem_u32(smem);
+        for (int i = threadIdx.x - 128; i < cols * 32; i += 256) {
+          const int c = rank * cols + (i >> 5), r = (i & 31) * 4;
+          float4 v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < S) v[q] = ld_dsmem_f4(base + (uint32_t)(c * 128 + r) * 4, q);
+#pragma unroll
+          for (int q = 1; q < 8; ++q) {
+            if (q < S) {
+              v[0].x += v[q].x;
+              v[0].y += v[q].y;
+              v[0].z += v[q].z;
+              v[0].w += v[q].w;
+            }
+          }
+          const int n = tl.n0 + r, m = tl.m0 + c;
+          if (m < tl.m_end) {
+            const float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+            __nv_bfloat16* y = p.y + (size_t)m * p.N + n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (n + j < p.N) y[j] = __float2bfloat16_rn(o[j] + (p.bias ? __bfloat162float(p.bias[n + j]) : 0.f));
           }
         }
       }

@@ -30,7 +30,7 @@ struct BlockPlan {
 template <int BN, bool G, bool X>
 cudaError_t skinny_attr() {
   cudaError_t e = cudaFuncSetAttribute(block_skinny_kernel<BN, G, X>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       SkinnyCfg<BN, G, X>::SMEM);
+                                       SkinnyCfg<BN, X>::SMEM);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(block_skinny_kernel<BN, G, X>, cudaFuncAttributePreferredSharedMemoryCarveout,
                              (int)cudaSharedmemCarveoutMaxShared);
@@ -78,35 +78,60 @@ bool quantizes(const dqgemm_s* h, int M) {
   return M <= 16 && h->k_stages * ceil_div((long long)std::min(h->E, M) * h->n_tiles, h->num_sms) <= 16;
 }
 
-// The split of K: the largest power of two S <= 8, S <= kb, with a CTA for each
-// of the T * S parts on an SM of its own (1 x 4096 x 4096, T = 32: S = 4 7.1 us,
-// S = 8 on half-shared SMs 7.6).  Tiles of up to 32 rows go to two CTAs an SM
-// where that still leaves each a long stream and half the SMs would have the
-// longest ones alone (1 x 14336 x 4096: S = 8 13.7 us, S = 4 14.6; but 1 x 4096
-// x 14336, T = 112: S = 2 14.1, S = 1 13.8), and where a call on bf16 quantizes
-// its few activations in each CTA, work that the split divides too (the same
-// call so: S = 2 15.3 us, S = 1 19.4; on codes as well, so that both add in one
-// order and give the same bits).
-int pick_split(const dqgemm_s* h, long long T, int bn, int M) {
+template <int BN>
+int skinny_clusters(int split) {
+  using C = SkinnyCfg<BN, false>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(split);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = split;
+  a[0].val.clusterDim.y = 1;
+  a[0].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, block_skinny_kernel<BN, false, false>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n;
+}
+
+// how many clusters of `split` CTAs run at once (they have to lie in one GPC
+// each, so not as many as the SMs would hold); asked once per handle
+int cluster_capacity(dqgemm_s* h, int bn, int split) {
+  int& c = h->max_clusters[bn == 16 ? 0 : bn == 32 ? 1 : bn == 64 ? 2 : 3][split];
+  if (c == 0) {
+    const int n = bn == 16 ? skinny_clusters<16>(split) : bn == 32 ? skinny_clusters<32>(split)
+                : bn == 64 ? skinny_clusters<64>(split) : skinny_clusters<128>(split);
+    c = n > 0 ? n : -1;
+  }
+  return c;
+}
+
+// The split of K: the largest power of two S <= 8, S <= kb, whose T clusters of
+// S CTAs all run at once (1 x 2048 x 2048, T = 16: S = 8 would take two turns,
+// 10.1 us against 4.7 at S = 4).
+int pick_split(dqgemm_s* h, long long T, int bn) {
   int s = 1;
   if (force_split() > 0) {
     while (2 * s <= std::min({force_split(), 8, h->k_stages})) s *= 2;
     return s;
   }
-  const auto may_double = [&](long long slots) { return s < 8 && 2 * s <= h->k_stages && T * 2 * s <= slots; };
-  while (may_double(h->num_sms)) s *= 2;
-  if (bn <= 32 && may_double(2ll * h->num_sms) &&
-      (quantizes(h, M) || (h->k_stages / (2 * s) >= 14 && 2 * T <= h->num_sms)))
-    s *= 2;
+  for (int c = 2; c <= 8 && c <= h->k_stages && T * c <= h->num_sms; c *= 2)
+    if (cluster_capacity(h, bn, c) >= T) s = c;
   return s;
 }
 
-BlockPlan dense_plan(const dqgemm_s* h, int M) {
+BlockPlan dense_plan(dqgemm_s* h, int M) {
   BlockPlan pl{};
   pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   if (M > 64) {
     const long long t1 = ceil_div(M, 128) * h->n_tiles, t2 = ceil_div(M, 256) * ceil_div(h->N, 256);
-    const int s = pick_split(h, t1, 128, M);
+    const int s = pick_split(h, t1, 128);
     const long long c1 = ceil_div(t1 * s, h->num_sms) * ceil_div(h->k_stages, s) * 520;
     const long long c2 = ceil_div(t2, h->num_sms / 2) * h->k_stages * 600;
     if (c2 <= c1) {
@@ -121,8 +146,8 @@ BlockPlan dense_plan(const dqgemm_s* h, int M) {
     pl.split = 1;
     pl.grid = 2 * (int)std::min<long long>(T, h->num_sms / 2);
   } else {
-    pl.split = pick_split(h, T, pl.bn, M);
-    pl.grid = (int)(pl.split > 1 ? T * pl.split : std::min<long long>(T, (long long)h->num_sms * (pl.bn <= 32 ? 2 : 1)));
+    pl.split = pick_split(h, T, pl.bn);
+    pl.grid = (int)(pl.split > 1 ? T * pl.split : std::min<long long>(T, h->num_sms));
   }
   return pl;
 }
@@ -199,7 +224,7 @@ cudaError_t launch(K kern, int grid, int threads, int smem, int cluster, const C
 template <int BN, bool G, bool X>
 cudaError_t launch_skinny(const BlockPlan& pl, const CUtensorMap& tw, const CUtensorMap& tx, const BlockParams& p,
                           cudaStream_t s) {
-  using C = SkinnyCfg<BN, G, X>;
+  using C = SkinnyCfg<BN, X>;
   return launch(block_skinny_kernel<BN, G, X>, pl.grid, C::THREADS, C::SMEM, pl.split, tw, tx, p, s);
 }
 
@@ -363,17 +388,16 @@ void block_fill_plan(dqgemm_handle h, int M, dqgemm_plan* pl) {
   pl->k_stages = h->k_stages;
   pl->grid = b.grid;
   pl->max_segments = b.split;
-  const bool g = h->experts;
   pl->stages = pl->x_stages = b.pair ? PairCfg::ST
-                              : b.bn == 16 ? (g ? SkinnyCfg<16, true, true>::ST : SkinnyCfg<16, false, true>::ST)
-                              : b.bn == 32 ? (g ? SkinnyCfg<32, true, false>::ST : SkinnyCfg<32, false, false>::ST)
-                              : b.bn == 64 ? SkinnyCfg<64, false, false>::ST
-                                           : SkinnyCfg<128, false, false>::ST;
+                              : b.bn == 16 ? SkinnyCfg<16, true>::ST
+                              : b.bn == 32 ? SkinnyCfg<32, false>::ST
+                              : b.bn == 64 ? SkinnyCfg<64, false>::ST
+                                           : SkinnyCfg<128, false>::ST;
   pl->smem_bytes = b.pair ? PairCfg::SMEM
-                   : b.bn == 16 ? (g ? SkinnyCfg<16, true, true>::SMEM : SkinnyCfg<16, false, true>::SMEM)
-                   : b.bn == 32 ? (g ? SkinnyCfg<32, true, false>::SMEM : SkinnyCfg<32, false, false>::SMEM)
-                   : b.bn == 64 ? SkinnyCfg<64, false, false>::SMEM
-                                : SkinnyCfg<128, false, false>::SMEM;
+                   : b.bn == 16 ? SkinnyCfg<16, true>::SMEM
+                   : b.bn == 32 ? SkinnyCfg<32, false>::SMEM
+                   : b.bn == 64 ? SkinnyCfg<64, false>::SMEM
+                                : SkinnyCfg<128, false>::SMEM;
   pl->workspace_bytes = x_workspace(h, M);
   pl->weight_bytes = h->weight_bytes;
   const long long T = (long long)pl->m_tiles * b.n_tiles;
