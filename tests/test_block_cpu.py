@@ -32,6 +32,7 @@ def test_run_refuses_null_arguments():
     lib = dq._native.lib()
     assert lib.dqgemm_run_fp8_block_quantized(None, 16, 16, 4, 16, None) == BAD
     assert lib.dqgemm_run_experts_quantized(None, 16, 16, 4, 16, 16, None) == BAD
+    assert lib.dqgemm_run_fp8_block(None, 16, 4, None, 16, None, 0, None) == BAD
 
 
 def test_python_layer_refuses_host_tensors():

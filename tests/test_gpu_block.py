@@ -373,3 +373,105 @@ def test_feed_forward_block_dense_and_by_experts():
     gq, gs = B.quantize_rows(B.silu_mul(h))
     ref = B.experts(gq, gs, down[0], down[1], off)
     assert np.linalg.norm(y.double().cpu().numpy() - ref) <= 0.02 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 512), (32, 4096, 1024), (100, 4096, 512), (1500, 2048, 4096), (16, 128, 128)])
+def test_wait_limit_expires_and_the_next_call_is_right(M, K, N):
+    # a limit so short that the first wait that does not complete at once gives
+    # up: no output, an error to read, and a layer and context that go on
+    _, q, s = rows(M, K, 121)
+    wq, ws = weights(1, N, K, 123)
+    lin = dq.QuantizedLinear("fp8_block", K, N, cuda(wq[0]), cuda(ws[0]))
+    q, s = cuda(q), cuda(s)
+    ref = lin.from_codes(q, scales=s)
+    out = torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    dq.dqgemm_set_wait_limit(lin.handle, 1)
+    lin.from_codes(q, scales=s, out=out)
+    torch.cuda.synchronize()
+    assert lin.last_error() == dq._native.DQ_ERR_TIMEOUT, lin.plan(M)
+    # a tile is written whole or not at all
+    o = out.float()
+    assert ((o == 5) | (o == ref.float())).all()
+    dq.dqgemm_set_wait_limit(lin.handle, 0)
+    assert torch.equal(lin.from_codes(q, scales=s, out=out), ref)
+    torch.cuda.synchronize()
+    assert lin.last_error() == 0
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 9], [300, 20, 700, 0]], ids=str)
+def test_experts_wait_limit_expires(counts):
+    E, K, N, M = len(counts), 1024, 512, sum(counts)
+    x, q, s = rows(M, K, 125)
+    wq, ws = weights(E, N, K, 127)
+    ex = dq.QuantizedExperts("fp8_block", E, K, N, cuda(wq), cuda(ws))
+    off = cuda(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    q, s = cuda(q), cuda(s)
+    ref = ex.from_codes(q, s, off)
+    dq.dqgemm_set_wait_limit(ex.handle, 1)
+    ex.from_codes(q, s, off)
+    ex(x.cuda(), off)
+    torch.cuda.synchronize()
+    assert ex.last_error() == dq._native.DQ_ERR_TIMEOUT
+    dq.dqgemm_set_wait_limit(ex.handle, 0)
+    assert torch.equal(ex.from_codes(q, s, off), ref)
+    assert torch.equal(ex(x.cuda(), off), ref)
+    torch.cuda.synchronize()
+    assert ex.last_error() == 0
+
+
+def test_offsets_past_32_bits():
+    # 4.6e9 weight bytes: the last experts' rows lie past 2^32
+    E, N, K, M = 70, 8192, 8192, 6
+    ex = dq.QuantizedExperts("fp8_block", E, K, N, torch.full((E, N, K), 0x38, dtype=torch.uint8, device="cuda"),
+                             torch.arange(1, E + 1, device="cuda", dtype=torch.float32)[:, None, None].expand(E, 64, 64).contiguous())
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:] = 2
+    off[E - 1:] = 4
+    off[E] = 6
+    x = torch.ones((M, K), dtype=torch.bfloat16, device="cuda")
+    y = ex(x, off.cuda()).float().cpu()        # 1.0 = code 0x38: y = K * expert
+    want = torch.tensor([1, 1, E - 1, E - 1, E, E]).float()[:, None] * K
+    assert (y == want.to(torch.bfloat16).float()).all()
+    ex.close()
+    # 2.5e9 outputs
+    M, N, K = 150016, 16384, 128
+    wq, ws = weights(1, 256, K, 131)
+    wide = cuda(wq[0]).repeat(N // 256, 1)
+    lin = dq.QuantizedLinear("fp8_block", K, N, wide, cuda(ws[0]).repeat(N // 256, 1))
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    tail, q, s = rows(5, K, 133)
+    x[-5:] = tail.cuda()
+    y = lin(x)
+    ref = B.linear(q, s, wq[0], ws[0])
+    check(y[-5:, -256:], ref, bound(q, s, wq[0], ws[0], ref))
+    assert not y[:-5:997].any() and torch.equal(y[-5:, :256], y[-5:, -256:])
+
+
+def test_static_codes_of_the_row_operators_feed_a_static_layer():
+    K, N, M = 512, 256, 40
+    torch.manual_seed(3)
+    w = torch.randn(N, K, device="cuda") * 0.05
+    x, r = randn((M, K), 141).to(torch.bfloat16).cuda(), randn((M, K), 142).to(torch.bfloat16).cuda()
+    lin = dq.QuantizedLinear.from_float("fp8_static", w, act_scale=0.01)
+    q, _ = dq.rmsnorm(x, residual=r, quant="fp8_static", s_out=0.01)
+    n, _ = dq.rmsnorm(x, residual=r)
+    y, y2 = lin.from_codes(q), lin(n)               # the second rounds the norm to bf16 first
+    assert (y.float() - y2.float()).norm() <= 0.02 * y2.float().norm()
+    g = torch.cat([x, r], 1)
+    y, y2 = lin.from_codes(dq.silu_mul(g, quant="fp8_static", s_out=0.01)), lin(dq.silu_mul(g))
+    assert (y.float() - y2.float()).norm() <= 0.02 * y2.float().norm()
+
+
+def test_quantize_replaces_linears_by_block_scaled_ones():
+    from weight_only_quantized_prologue_b200 import module as Mod
+
+    torch.manual_seed(5)
+    model = torch.nn.Sequential(torch.nn.Linear(256, 384), torch.nn.ReLU(), torch.nn.Linear(384, 64))
+    model = model.to(device="cuda", dtype=torch.bfloat16)
+    w = [(m.weight.float(), m.bias.detach()) for m in (model[0], model[2])]
+    l1, l2 = (dq.QuantizedLinear.from_float("fp8_block", a, b) for a, b in w)
+    Mod.quantize_(model, "fp8_block")
+    x = randn((3, 7, 256), 151).to(torch.bfloat16).cuda()
+    with torch.no_grad():
+        y = model(x)
+    assert torch.equal(y, l2(torch.relu(l1(x.view(-1, 256)))).view(3, 7, 64))

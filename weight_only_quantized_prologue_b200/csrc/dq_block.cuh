@@ -157,7 +157,26 @@ __device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, const
       if (mbar_try_wait(bar, parity)) return true;
   }
 }
-// whether three barriers have all completed their phases, looked at together
+// whether four barriers have all completed their phases, looked at together
+__device__ __forceinline__ bool mbar_try_wait4(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc,
+                                               uint64_t* d, uint32_t pd) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r, s;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 s, [%7], %8;\n\t"
+      "and.pred p, p, q;\n\t"
+      "and.pred r, r, s;\n\t"
+      "and.pred p, p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb), "r"(smem_u32(c)), "r"(pc), "r"(smem_u32(d)), "r"(pd)
+      : "memory");
+  return ok != 0;
+}
+// ... or three
 __device__ __forceinline__ bool mbar_try_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
   uint32_t ok;
   asm volatile(
@@ -285,8 +304,8 @@ __device__ __forceinline__ void load_scales(const float* row, bool live, int b, 
 // own, [SR][BN].  It needs no barrier against reuse: who writes entry i + SR
 // has seen the MMAs of block i + SR - ST done, hence those of block i + PB,
 // which were issued after the epilogue had finished with block i.  The MMAs
-// of a block wait for its scales too (through full_x): nobody falls a whole
-// phase of a barrier behind, where a parity would be taken for the next.
+// of a block wait for its scales too: nobody falls a whole phase of a barrier
+// behind, where a parity would be taken for the next.
 // ---------------------------------------------------------------------------
 template <int BN, bool XBF>
 struct SkinnyCfg {
@@ -414,7 +433,7 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(&full_w[s], 1);
-      mbar_init(&full_x[s], XBF ? 1 : 2);   // a quantizing warp, or copies and scales
+      mbar_init(&full_x[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < C::PB; ++b) {
@@ -524,10 +543,7 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
           for (int j = 0; j < CPL; ++j)
             if (lane + 32 * j < BN) scales[e * BN + lane + 32 * j] = c[j][i];
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full_x[s]);
-            mbar_arrive(&sc_full[e]);
-          }
+          if (lane == 0) mbar_arrive(&sc_full[e]);
           ++it;
           if (++s == C::ST) { s = 0; ph ^= 1; }
           if (++e == C::SR) e = 0;
@@ -575,14 +591,14 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (elect_one()) {
-      int s = 0, pb = 0;
-      uint32_t ph = 0, pph = 0;
+      int s = 0, pb = 0, e = 0;
+      uint32_t ph = 0, pph = 0, eph = 0;
       bool ok = true, issued = false;
       for (int t = t0; ok && t < tiles; t += step) {
         for (int b = b0; b < b1; ++b) {
-          if (!mbar_try_wait3(&full_w[s], ph, &full_x[s], ph, &acc_empty[pb], pph ^ 1) &&
+          if (!mbar_try_wait4(&full_w[s], ph, &full_x[s], ph, &sc_full[e], eph, &acc_empty[pb], pph ^ 1) &&
               (!block_wait(&full_w[s], ph, ctl()) || !block_wait(&full_x[s], ph, ctl()) ||
-               !block_wait(&acc_empty[pb], pph ^ 1, ctl()))) { ok = false; break; }
+               !block_wait(&sc_full[e], eph, ctl()) || !block_wait(&acc_empty[pb], pph ^ 1, ctl()))) { ok = false; break; }
           tc_fence_after();
           const uint32_t wb = smem_u32(smem + s * C::STAGE), xb = wb + C::W_BYTES;
 #pragma unroll
@@ -593,6 +609,7 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
           tc_commit(&acc_full[pb]);
           if (++s == C::ST) { s = 0; ph ^= 1; }
           if (++pb == C::PB) { pb = 0; pph ^= 1; }
+          if (++e == C::SR) { e = 0; eph ^= 1; }
         }
       }
       if (issued) {

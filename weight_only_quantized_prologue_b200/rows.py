@@ -123,11 +123,15 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out
     output (see the module); with a residual also the new one, r rounded to
     x's type, as the last of a tuple.  ``residual_out`` may be ``residual``
     itself, or a contiguous x."""
-    M, K, ld = _rows(x, "x")
+    dt = x.dtype
+    if x.dim() == 2 and x.is_cuda and dt in _TYPES and x.is_contiguous() and x.shape[1]:
+        M, K = x.shape       # the common operand, checked in place
+        ld = K
+    else:
+        M, K, ld = _rows(x, "x")
     dev = x.get_device()
     if _one_device is not True:
         check_current(dev)
-    dt = x.dtype
     wt = wp = rp = np = None
     if weight is not None:
         wt = _TYPES.get(weight.dtype)
