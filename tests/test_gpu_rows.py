@@ -170,6 +170,11 @@ def test_strided_rows_and_given_outputs():
     assert got[0] is out and got[1] is sc and got[2] is r
     for a, b in zip(ref, got):
         assert torch.equal(a, b)
+    # many rows a CTA, the new residual in the place of x
+    x, r = gen((5000, 520), 20, "bf16"), gen((5000, 520), 21, "bf16")
+    ref = dq.rmsnorm(x, residual=r)
+    got = dq.rmsnorm(x, residual=r, residual_out=x)
+    assert got[1] is x and all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
 @pytest.mark.parametrize("K", [256, 200])

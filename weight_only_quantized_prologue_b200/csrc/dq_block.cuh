@@ -759,6 +759,11 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// Arrive on the leader's barrier.  Relaxed: what it orders are tensor memory
+// reads, complete at their wait and fenced by tcgen05.fence, and shared memory
+// that the copy engine filled; a release at cluster scope waits for all of the
+// thread's memory operations (the epilogue's block of K took 1300 cycles so,
+// 425 without).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }

@@ -332,11 +332,13 @@ dqgemm_status block_create(dqgemm_handle* out, bool experts, int E, int K, int N
   }
   *h->status_host = 0;
   e = cudaHostGetDevicePointer(reinterpret_cast<void**>(&h->status), h->status_host, 0);
-  // codes and scales the GPU finds outside the format are counted in the status word
+  // (the buffers may still be being written, on whatever stream)
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(h->wchunks, packed_w, wb, cudaMemcpyDeviceToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(h->col_scale, scales, ns * 4, cudaMemcpyDeviceToDevice);
   if (e == cudaSuccess && bias) e = cudaMemcpy(h->bias, bias, rows * 2, cudaMemcpyDeviceToDevice);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  // codes and scales outside the format are noted in the status word
   if (e == cudaSuccess) {
     check_fp8_block_kernel<<<h->num_sms * 4, 256>>>(h->wchunks, wb, h->col_scale, ns, h->status);
     e = cudaGetLastError();

@@ -49,12 +49,18 @@ int sm_count() {
   return counts[dev];
 }
 
-// threads a multiprocessor that a launch over many rows starts: each keeps the
-// loads of its next vectors in flight
-#ifndef ROW_THREADS
-#define ROW_THREADS 1024
-#endif
-constexpr int kRowThreads = ROW_THREADS;
+// CTAs of a kernel that are resident at once, on all multiprocessors: what a
+// launch over many rows starts, since each goes on to the next rows itself
+template <typename K>
+long long resident_ctas(K kern, int threads, int (&cache)[17]) {
+  int& n = cache[threads / 32];   // (every thread would write the same value)
+  if (n == 0) {
+    int v = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, 0) != cudaSuccess) cudaGetLastError();
+    n = std::max(1, v);
+  }
+  return (long long)n * sm_count();
+}
 
 template <typename... KArgs, typename... Args>
 dqgemm_status launch_rows(void (*kern)(KArgs...), dim3 grid, dim3 block, void* stream, Args... args) {
@@ -70,19 +76,26 @@ dqgemm_status launch_rows(void (*kern)(KArgs...), dim3 grid, dim3 block, void* s
   return cuda_err(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...));
 }
 
+template <typename T, int NV, int OUT, int AL, int MT>
+dqgemm_status norm_grid(const RowArgs& a, long long need, dim3 block, void* stream) {
+  static int cache[17] = {};
+  const long long most = resident_ctas(rmsnorm_kernel<T, NV, OUT, AL, MT>, (int)(block.x * block.y), cache);
+  return launch_rows(rmsnorm_kernel<T, NV, OUT, AL, MT>, dim3((unsigned)std::min(need, most)), block, stream, a);
+}
+
 template <typename T, int OUT, int AL>
 dqgemm_status norm_launch(const RowArgs& a, void* stream) {
-  // threads a row: one vector each up to 512 of them (K = 8192), then two;
-  // rows past K = 16384 are read twice
-  const int vecs = (a.K + 15) / 16;
-  const int tpr = std::min(512, (vecs + 31) / 32 * 32);
-  const int per = (vecs + tpr - 1) / tpr;
+  // threads a row: one vector each up to 512 of them (K = 8192: 82.8 us for
+  // 8192 rows, with two each on half the threads 88.0), then two; rows past
+  // K = 16384 are read twice
+  const int vecs = (a.K + 15) / 16, per = vecs <= 512 ? 1 : 2;
+  const int tpr = std::min(512, ((vecs + per - 1) / per + 31) / 32 * 32);
   const int rows = std::max(1, 128 / tpr);
   const dim3 block(tpr, rows);
-  const int ctas = (int)std::min<long long>((a.M + (long long)rows - 1) / rows, (long long)sm_count() * (kRowThreads / (tpr * rows)));
-  if (per <= 1) return launch_rows(rmsnorm_kernel<T, 1, OUT, AL>, dim3(ctas), block, stream, a);
-  if (per <= 2) return launch_rows(rmsnorm_kernel<T, 2, OUT, AL>, dim3(ctas), block, stream, a);
-  return launch_rows(rmsnorm_kernel<T, 0, OUT, AL>, dim3(ctas), block, stream, a);
+  const long long need = (a.M + (long long)rows - 1) / rows;
+  if (per == 1)
+    return tpr <= 256 ? norm_grid<T, 1, OUT, AL, 256>(a, need, block, stream) : norm_grid<T, 1, OUT, AL, 512>(a, need, block, stream);
+  return vecs <= 1024 ? norm_grid<T, 2, OUT, AL, 512>(a, need, block, stream) : norm_grid<T, 0, OUT, AL, 512>(a, need, block, stream);
 }
 
 template <typename T, bool GATE, int OUT, int AL>
@@ -91,7 +104,8 @@ dqgemm_status plain_launch(const RowArgs& a, void* stream) {
   const long long items = (long long)parts * a.M;
   // (few warps: one a CTA, so that they spread over the multiprocessors)
   const int per = (int)std::max<long long>(1, std::min<long long>(8, items / sm_count()));
-  const int ctas = (int)std::min<long long>((items + per - 1) / per, (long long)sm_count() * (kRowThreads / (32 * per)));
+  static int cache[17] = {};
+  const int ctas = (int)std::min((items + per - 1) / per, resident_ctas(rows_kernel<T, GATE, OUT, AL>, 32 * per, cache));
   return launch_rows(rows_kernel<T, GATE, OUT, AL>, dim3(ctas), dim3(32 * per), stream, a, parts);
 }
 
