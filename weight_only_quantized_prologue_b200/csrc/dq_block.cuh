@@ -157,26 +157,7 @@ __device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, const
       if (mbar_try_wait(bar, parity)) return true;
   }
 }
-// whether four barriers have all completed their phases, looked at together
-__device__ __forceinline__ bool mbar_try_wait4(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc,
-                                               uint64_t* d, uint32_t pd) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q, r, s;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 s, [%7], %8;\n\t"
-      "and.pred p, p, q;\n\t"
-      "and.pred r, r, s;\n\t"
-      "and.pred p, p, r;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb), "r"(smem_u32(c)), "r"(pc), "r"(smem_u32(d)), "r"(pd)
-      : "memory");
-  return ok != 0;
-}
-// ... or three
+// whether three barriers have all completed their phases, looked at together
 __device__ __forceinline__ bool mbar_try_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
   uint32_t ok;
   asm volatile(
@@ -304,8 +285,8 @@ __device__ __forceinline__ void load_scales(const float* row, bool live, int b, 
 // own, [SR][BN].  It needs no barrier against reuse: who writes entry i + SR
 // has seen the MMAs of block i + SR - ST done, hence those of block i + PB,
 // which were issued after the epilogue had finished with block i.  The MMAs
-// of a block wait for its scales too: nobody falls a whole phase of a barrier
-// behind, where a parity would be taken for the next.
+// of a block wait for its scales too (through full_x): nobody falls a whole
+// phase of a barrier behind, where a parity would be taken for the next.
 // ---------------------------------------------------------------------------
 template <int BN, bool XBF>
 struct SkinnyCfg {
@@ -433,7 +414,7 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(&full_w[s], 1);
-      mbar_init(&full_x[s], 1);
+      mbar_init(&full_x[s], XBF ? 1 : 2);   // a quantizing warp, or copies and scales
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < C::PB; ++b) {
@@ -543,7 +524,10 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
           for (int j = 0; j < CPL; ++j)
             if (lane + 32 * j < BN) scales[e * BN + lane + 32 * j] = c[j][i];
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_full[e]);
+          if (lane == 0) {
+            mbar_arrive(&full_x[s]);
+            mbar_arrive(&sc_full[e]);
+          }
           ++it;
           if (++s == C::ST) { s = 0; ph ^= 1; }
           if (++e == C::SR) e = 0;
@@ -591,14 +575,14 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (elect_one()) {
-      int s = 0, pb = 0, e = 0;
-      uint32_t ph = 0, pph = 0, eph = 0;
+      int s = 0, pb = 0;
+      uint32_t ph = 0, pph = 0;
       bool ok = true, issued = false;
       for (int t = t0; ok && t < tiles; t += step) {
         for (int b = b0; b < b1; ++b) {
-          if (!mbar_try_wait4(&full_w[s], ph, &full_x[s], ph, &sc_full[e], eph, &acc_empty[pb], pph ^ 1) &&
+          if (!mbar_try_wait3(&full_w[s], ph, &full_x[s], ph, &acc_empty[pb], pph ^ 1) &&
               (!block_wait(&full_w[s], ph, ctl()) || !block_wait(&full_x[s], ph, ctl()) ||
-               !block_wait(&sc_full[e], eph, ctl()) || !block_wait(&acc_empty[pb], pph ^ 1, ctl()))) { ok = false; break; }
+               !block_wait(&acc_empty[pb], pph ^ 1, ctl()))) { ok = false; break; }
           tc_fence_after();
           const uint32_t wb = smem_u32(smem + s * C::STAGE), xb = wb + C::W_BYTES;
 #pragma unroll
@@ -609,7 +593,6 @@ __global__ void __launch_bounds__(SkinnyCfg<BN, XBF>::THREADS, 1)
           tc_commit(&acc_full[pb]);
           if (++s == C::ST) { s = 0; ph ^= 1; }
           if (++pb == C::PB) { pb = 0; pph ^= 1; }
-          if (++e == C::SR) { e = 0; eph ^= 1; }
         }
       }
       if (issued) {
@@ -759,11 +742,6 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// Arrive on the leader's barrier.  Relaxed: what it orders are tensor memory
-// reads, complete at their wait and fenced by tcgen05.fence, and shared memory
-// that the copy engine filled; a release at cluster scope waits for all of the
-// thread's memory operations (the epilogue's block of K took 1300 cycles so,
-// 425 without).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -778,6 +756,19 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// a look at a barrier whose answer is used later
+__device__ __forceinline__ uint32_t mbar_peek(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok;
+}
 
 struct PairCfg {
   static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
@@ -797,9 +788,9 @@ struct PairCfg {
   static constexpr int THREADS = 384;   // 4 warps of copies and MMAs, 8 of sums
   // M = 256, N = 256, e4m3 x e4m3 -> f32
   static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-  // registers: 128 threads at 40, 256 at 216, out of the launch's 384 x 168
-  static constexpr int REGS_LOW = 40, REGS_HIGH = 216;
-  static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 160, "register split");
+  // registers: 128 threads at 64 (fewer spill), 256 at 208, out of the launch's 384 x 168
+  static constexpr int REGS_LOW = 64, REGS_HIGH = 208;
+  static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 168, "register split");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -934,49 +925,54 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
     if constexpr (!GROUPED) pdl_wait();
     const int qd = warp & 3, h = (warp - 4) >> 2;   // 32 rows x half h of the tile's columns
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
+    uint32_t ready = 0;   // the next block's partial was complete when last looked at
     const uint32_t empty_addr = dsmem_addr(acc_empty, 0);
     int pb = 0;
     uint32_t pph = 0;
     bool ok = true;
     for (int t = t0; ok && t < tiles; t += step) {
-      const BlockTile tl = block_tile<256, 256, GROUPED>(p, start, t);
-      const int m = tl.m0 + rank * 128 + qd * 32 + lane, n0 = tl.n0 + h * 128;
-      const bool live = m < tl.m_end;
-      const bool live_n = n0 < p.N;
-      const float* sxr = p.sx + (size_t)(live ? m : 0) * p.kb;
-      const float* sw = p.sw + ((size_t)tl.e * p.nb + (live_n ? n0 >> 7 : 0)) * p.kb;
-      float nx[4], nw[4], sc[4];
-      load_scales(sxr, live, 0, p.kb, nx);
-      load_scales(sw, live_n, 0, p.kb, nw);
+      const float *sxr, *sw;
+      bool live, live_n;   // this row and half exist
+      {
+        const BlockTile tl = block_tile<256, 256, GROUPED>(p, start, t);
+        const int m = tl.m0 + rank * 128 + qd * 32 + lane, n0 = tl.n0 + h * 128;
+        live = m < tl.m_end;
+        live_n = n0 < p.N;
+        sxr = p.sx + (size_t)(live ? m : 0) * p.kb;
+        sw = p.sw + ((size_t)tl.e * p.nb + (live_n ? n0 >> 7 : 0)) * p.kb;
+      }
+      // (the next block's scales are fetched while this one is summed: mostly
+      // from L1, a row's 32 consecutive blocks share a line)
+      float nx = live ? sxr[0] : 0.f, nw = live_n ? sw[0] : 0.f;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      for (int bg = 0; ok && bg < p.kb; bg += 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i] = nx[i] * nw[i];
-        load_scales(sxr, live, bg + 4, p.kb, nx);
-        load_scales(sw, live_n, bg + 4, p.kb, nw);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (bg + i >= p.kb) break;
-          if (!block_wait_warp(&acc_full[h * 2 + pb], pph, ctl())) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t ta = tmem + lane_base + pb * 256 + h * 128;
-#pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 16) {
-            float v[16];
-            tmem_ld_n<16>(ta + c0, v);
-            tmem_wait_regs<16>(v);
-            if (c0 + 16 == 128) {   // the buffer is free as soon as the last columns have arrived
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(empty_addr + (h * 2 + pb) * 8);
-            }
-#pragma unroll
-            for (int c = 0; c < 16; ++c) acc[c0 + c] = fmaf(v[c], sc[i], acc[c0 + c]);
-          }
-          if (++pb == C::PB) { pb = 0; pph ^= 1; }
+      for (int b = 0; b < p.kb; ++b) {
+        const float s1 = nx * nw;
+        if (b + 1 < p.kb) {
+          if (live) nx = sxr[b + 1];
+          if (live_n) nw = sw[b + 1];
         }
+        if (!__all_sync(0xFFFFFFFFu, ready) && !block_wait_warp(&acc_full[h * 2 + pb], pph, ctl())) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t ta = tmem + lane_base + pb * 256 + h * 128;
+        uint64_t* next_bar = &acc_full[h * 2 + (pb ^ 1)];
+        const uint32_t next_par = pb ? pph ^ 1 : pph;
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 16) {
+          float v[16];
+          tmem_ld_n<16>(ta + c0, v);
+          tmem_wait_regs<16>(v);
+          if (c0 + 16 == 128) {   // the buffer is free as soon as the last columns have arrived
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_addr + (h * 2 + pb) * 8);
+            ready = mbar_peek(next_bar, next_par);   // (its answer arrives during the last sums)
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) acc[c0 + c] = fmaf(v[c], s1, acc[c0 + c]);
+        }
+        if (++pb == C::PB) { pb = 0; pph ^= 1; }
       }
       if (!ok) break;
       // Out through shared memory: each thread leaves its row there and hands
@@ -984,6 +980,10 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
       // (stores from the registers touch 32 rows an instruction: 5000 cycles
       // a tile against 32 x 512 of MMAs).
       if (live_n) {
+        // (where the tile lies is found again: kept over the sums it would cost
+        // registers that they have not)
+        const BlockTile tl = block_tile<256, 256, GROUPED>(p, start, t);
+        const int m = tl.m0 + rank * 128 + qd * 32 + lane, n0 = tl.n0 + h * 128;
         const __nv_bfloat16* bias = p.bias ? p.bias + (size_t)tl.e * p.N + n0 : nullptr;
         const int nn = min(128, p.N - n0);
         uint8_t* mine = smem + C::OUT_OFF + (threadIdx.x - 128) * C::OUT_PITCH;
