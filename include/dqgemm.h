@@ -183,7 +183,8 @@ dqgemm_status dqgemm_run_fp8_static_quantized(dqgemm_handle h, const void* q, in
  * q_out[m, n] = e4m3(f32(y[m, n]) / s_out) with y the bf16 result, IEEE
  * division, round to nearest even, saturating -- the codes
  * dqgemm_quantize_act_fp8(y, s_out) would give.  q_out: device u8 [M, N],
- * 16-byte aligned; s_out > 0 (DQ_ERR_INVALID_ARG otherwise).  Any format. */
+ * 16-byte aligned; s_out > 0 (DQ_ERR_INVALID_ARG otherwise).  Any format but
+ * the W4A4 and block-scaled ones (DQ_ERR_UNSUPPORTED). */
 dqgemm_status dqgemm_run_quantized_out(dqgemm_handle h, const void* x, int M, void* q_out, float s_out,
                                        void* stream);
 
@@ -421,7 +422,7 @@ dqgemm_status dqgemm_selftest_timeout(int timeout_us, void* stream);
 typedef struct {
   int bn;               /* MMA N (activation rows per tile): 16, 32, 64 or 128 */
   int m_tiles;          /* ceil(M / bn) */
-  int n_tiles;          /* ceil(N / 128) */
+  int n_tiles;          /* ceil(N / 128) (block-scaled with bn = 256: ceil(N / 256)) */
   int k_stages;         /* ceil(K / 128) */
   int grid;             /* CTAs launched (<= number of SMs) */
   int max_segments;     /* most CTAs sharing one output tile (split-K depth) */

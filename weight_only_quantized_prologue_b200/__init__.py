@@ -366,8 +366,10 @@ class QuantizedExperts:
     _out = QuantizedLinear._out
 
     def _check_offsets(self, offsets):
-        torch = _torch()
-        _require(offsets, "offsets", shape=(self.E + 1,), dtype=torch.int32, device=self.device)
+        t = offsets
+        if not (getattr(t, "dtype", None) is _torch().int32 and t.is_cuda and t.dim() == 1 and t.shape[0] == self.E + 1
+                and t.is_contiguous() and t.get_device() == self._dev):
+            _require(t, "offsets", shape=(self.E + 1,), dtype=_torch().int32, device=self.device)
 
     def __call__(self, x, offsets, out=None, stream=None):
         """y[m] = x[m] . deq(W_e)^T + b_e for offsets[e] <= m < offsets[e + 1];
@@ -386,7 +388,8 @@ class QuantizedExperts:
         """The same on e4m3 codes uint8 [M, K] with scales fp32 [M, ceil(K / 128)]."""
         torch = _torch()
         M = self._check_x(q, torch.uint8, "q")
-        _require(scales, "scales", shape=(M, (self.K + 127) // 128), dtype=torch.float32, device=self.device)
+        if not _fits(scales, (self.K + 127) // 128, torch.float32, M, self._dev):
+            _require(scales, "scales", shape=(M, (self.K + 127) // 128), dtype=torch.float32, device=self.device)
         self._check_offsets(offsets)
         out = self._out(out, M, torch.bfloat16)
         if M:

@@ -13,7 +13,8 @@ output:
                   an "fp8_static" layer calibrated with that scale takes
 
 Results are allocated if not given (``out``, ``scales``, ``residual_out``) and
-must not overlap the inputs, except where a function says so.  A call runs on
+must not overlap the inputs, except where a function says so.  Inference only:
+no gradient is recorded.  A call runs on
 ``stream``, or on the current stream of the tensors' device, which must be the
 current device.
 """
@@ -25,6 +26,8 @@ import torch
 from . import _native, _require
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # _native.ROW_TYPES, ROW_OUTS
+_U8, _F32 = torch.uint8, torch.float32
+_empty = torch.empty_strided   # (the cheapest of torch's allocating calls on the host)
 _one_device = None
 
 
@@ -41,6 +44,13 @@ def check_current(dev):
 
 def _rows(x, name, halves=1):
     """(M, K, row stride) of a 2-D operand whose rows are contiguous."""
+    try:                     # the common operand, checked in a few steps
+        if x.is_cuda and x.dtype in _TYPES and x.is_contiguous():
+            M, width = x.shape
+            if width and not width % halves:
+                return M, width // halves, width
+    except (AttributeError, ValueError):
+        pass
     if getattr(x, "dim", lambda: 0)() != 2:
         raise ValueError(f"{name} must be 2-D")
     if not x.is_cuda:
@@ -51,8 +61,6 @@ def _rows(x, name, halves=1):
     if width % halves or width == 0:
         raise ValueError(f"{name} must hold {halves} halves of at least one column" if halves > 1
                          else f"{name} must have at least one column")
-    if x.is_contiguous():
-        return M, width // halves, width
     ld, inner = x.stride()
     if (inner != 1 and width != 1) or (M > 1 and ld < width):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
@@ -60,8 +68,7 @@ def _rows(x, name, halves=1):
 
 
 def _new(x, M, K, dtype):
-    # (empty_strided: the cheapest of torch's allocating calls on the host)
-    return torch.empty_strided((M, K), (K, 1), dtype=dtype, device=x.device)
+    return _empty((M, K), (K, 1), dtype=dtype, device=x.device)
 
 
 def _given(t, name, M, K, dtype, x):
@@ -79,15 +86,16 @@ def _outputs(x, M, K, quant, s_out, out_dtype, out, scales):
             raise ValueError("out_dtype goes with quant=None")
         if s_out is not None:
             raise ValueError("s_out goes with quant='fp8_static'")
+        dev = x.device
         if out is None:
-            out = _new(x, M, K, torch.uint8)
+            out = _empty((M, K), (K, 1), dtype=_U8, device=dev)
         else:
-            _given(out, "out", M, K, torch.uint8, x)
+            _given(out, "out", M, K, _U8, x)
         kb = (K + 127) // 128
         if scales is None:
-            scales = _new(x, M, kb, torch.float32)
+            scales = _empty((M, kb), (kb, 1), dtype=_F32, device=dev)
         else:
-            _given(scales, "scales", M, kb, torch.float32, x)
+            _given(scales, "scales", M, kb, _F32, x)
         return 3, 1.0, out, scales
     if scales is not None:
         raise ValueError("scales go with quant='fp8_block'")
@@ -123,12 +131,8 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out
     output (see the module); with a residual also the new one, r rounded to
     x's type, as the last of a tuple.  ``residual_out`` may be ``residual``
     itself, or a contiguous x."""
+    M, K, ld = _rows(x, "x")
     dt = x.dtype
-    if x.dim() == 2 and x.is_cuda and dt in _TYPES and x.is_contiguous() and x.shape[1]:
-        M, K = x.shape       # the common operand, checked in place
-        ld = K
-    else:
-        M, K, ld = _rows(x, "x")
     dev = x.get_device()
     if _one_device is not True:
         check_current(dev)
@@ -173,9 +177,11 @@ def silu_mul(x, quant=None, s_out=None, out_dtype=None, out=None, scales=None, s
         check_current(dev)
     kind, s_out, out, scales = _outputs(x, M, K, quant, s_out, out_dtype, out, scales)
     if M:
-        _native._check(_native.lib().dqgemm_silu_mul(
-            _TYPES[x.dtype], x.data_ptr(), ld, M, K, kind, s_out, out.data_ptr(),
-            None if scales is None else scales.data_ptr(), _native.device_stream(stream, dev)), "dqgemm_silu_mul")
+        st = _native.lib().dqgemm_silu_mul(_TYPES[x.dtype], x.data_ptr(), ld, M, K, kind, s_out, out.data_ptr(),
+                                           None if scales is None else scales.data_ptr(),
+                                           _native.device_stream(stream, dev))
+        if st:
+            raise _native.DQError(st, "dqgemm_silu_mul")
     return out if scales is None else (out, scales)
 
 
