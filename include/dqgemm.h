@@ -311,7 +311,9 @@ dqgemm_status dqgemm_quantize_act_fp4(dqgemm_format fmt, const void* x, int M, i
  *       s_out takes (dqgemm_run_fp8_static_quantized); s_out finite and > 0
  * Buffers need their natural alignment only; rows aligned to 32 bytes (16 for
  * codes) with K % 16 == 0, or to half of that with K % 8 == 0, are moved in
- * vectors, others element by element.
+ * vectors as they lie; others in the aligned 16-byte pieces that they touch,
+ * so that bytes between the rows of x may be read (and are not used), but
+ * none before x or behind its last row.
  * M >= 1, 1 <= K <= 2^28.  One launch on `stream`, no allocation, no
  * synchronization; programmatic dependent launch as dqgemm_run, and nothing
  * is read or written before the previous kernel of the stream has completed. */

@@ -177,6 +177,49 @@ def test_strided_rows_and_given_outputs():
     assert got[1] is x and all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
+@pytest.mark.parametrize("dt,odt", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp16"), ("fp32", "fp32"), ("bf16", "fp8_block")])
+@pytest.mark.parametrize("K", [1, 3, 7, 15, 17, 129, 511, 515, 1031, 4100])
+def test_rows_that_start_anywhere(dt, odt, K):
+    """Every offset of each buffer from a 16-byte boundary gives the same bits,
+    and nothing beside the outputs is written."""
+    M, gap = 3, 5
+    quant = odt if odt == "fp8_block" else None
+    ot = torch.uint8 if quant else DT[odt]
+    xv, rv, w = gen((M, 2 * K), 1, dt), gen((M, K), 2, dt), gen((K,), 3, dt)
+
+    def place(v, at, ld):                      # v [M, cols] with rows ld apart, `at` elements into its buffer
+        buf = torch.full((at + ld * M,), 9.0, dtype=v.dtype, device="cuda")
+        view = buf.as_strided(v.shape, (ld, 1), at)
+        view.copy_(v)
+        return view
+
+    def empty(t, at):                          # [M, K] inside a buffer of a known value
+        buf = torch.full((at + M * K + 40,), 77, dtype=t, device="cuda")
+        return buf, buf[at:at + M * K].view(M, K)
+
+    first = None
+    for at in range(17):
+        x, g = place(xv[:, :K], at, K + gap), place(xv, at, 2 * K + gap)
+        res = place(rv, (3 * at) % 17, K)
+        wt = place(w.view(1, K), (5 * at) % 17, K).view(K)
+        outs = [empty(ot, (7 * at) % 17), empty(ot, (11 * at) % 17), empty(DT[dt], at)]
+        kw = dict(quant=quant) if quant else dict(out_dtype=ot)
+        got = dq.rmsnorm(x, wt, residual=res, out=outs[0][1], residual_out=outs[2][1], **kw)
+        gate = dq.silu_mul(g, out=outs[1][1], **kw)
+        all_ = list(got) + (list(gate) if quant else [gate])
+        same = dq.rmsnorm(x, wt, residual=res, residual_out=res, **kw)   # in place
+        all_ += list(same)
+        if quant:
+            all_ += list(dq.quantize_act_fp8_block(x, out=empty(ot, at)[1]))
+        bits = [t.contiguous().clone().view(torch.uint8) for t in all_]
+        for (buf, view), o in zip(outs, ((7 * at) % 17, (11 * at) % 17, at)):
+            assert (buf[:o] == 77).all() and (buf[o + M * K:] == 77).all()
+        if first is None:
+            first = bits
+        for a, b in zip(first, bits):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("K", [256, 200])
 def test_special_values(K):
     x = gen((6, K), 15, "fp32")

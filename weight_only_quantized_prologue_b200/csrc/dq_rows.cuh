@@ -33,6 +33,7 @@ struct RowArgs {
   long long ldx;
   const void* res;        // rmsnorm: residual [M, K] or null
   void* res_out;          //   x + residual, rounded to the input type (null without a residual)
+  long long x_bytes, row_bytes;   // extents of x (gaps between its rows included) and of the residual
   const void* w;          //   weight [K] or null (ones)
   int w_type;             //   its RowType
   float eps;
@@ -46,7 +47,12 @@ struct RowArgs {
 // 16 consecutive elements <-> fp32, n of which exist (n <= 0: none); missing
 // ones read as 0.  AL = 2: rows are 32-byte aligned and K is a multiple of 16,
 // so a vector is whole; 1: 16-byte aligned and a multiple of 8, so each half
-// is; 0: element by element.
+// is; 0: rows start anywhere.  A vector of those is read in the aligned
+// 16-byte pieces that it touches and shifted into place, and written in
+// aligned pieces that neighbouring lanes put together (element by element,
+// a norm of 8192 x 4099 in bf16 took 283 us, now 88, a gated SiLU of 4096 x 5003
+// 128 us, now 23).  Only pieces that lie within
+// the tensor are touched; at its ends it is elements.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -118,15 +124,60 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// a vector as it lies in memory (AL = 0: its elements' bits one a word)
+// N words from byte `off` (0 to 15, a multiple of SIZE) of t on.  `off` is the
+// same for a whole warp: a branch on its words costs less than selects (about
+// 11 instructions against 27 for 8 words).
+template <int N, int SIZE>
+__device__ __forceinline__ void shift_words(const uint32_t (&t)[N + 4], uint32_t off, uint32_t (&w)[N]) {
+  const auto from = [&](auto words) {
+    constexpr int D = decltype(words)::value;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = SIZE == 4 ? t[i + D] : __funnelshift_r(t[i + D], t[i + D + 1], (off & 3) * 8);
+  };
+  if (off < 8) {
+    if (off < 4) from(std::integral_constant<int, 0>());
+    else from(std::integral_constant<int, 1>());
+  } else {
+    if (off < 12) from(std::integral_constant<int, 2>());
+    else from(std::integral_constant<int, 3>());
+  }
+}
+
+// a vector as it lies in memory
 template <int AL, typename T>
 struct Raw16 {
-  static constexpr int WORDS = AL == 0 ? 16 : 4 * sizeof(T);
+  static constexpr int PACKED = 4 * sizeof(T);               // words of 16 elements
+  static constexpr int WORDS = AL == 0 ? PACKED + 4 : PACKED;
   uint32_t w[WORDS];
-  __device__ __forceinline__ void load(const T* p, int n) {
+  uint32_t off;   // AL = 0: bytes of w before the vector
+  int left;       //         elements that exist
+  // begin, bytes: the tensor that p points into
+  __device__ __forceinline__ void load(const T* p, int n, const void* begin, long long bytes) {
     if constexpr (AL == 0) {
+      left = n;
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p), piece = at & ~uintptr_t(15), lo_end = reinterpret_cast<uintptr_t>(begin);
+      off = (uint32_t)(at & 15);
+      if (n > 0 && piece >= lo_end && piece + 4 * WORDS <= lo_end + bytes) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = i < n ? bits(p[i]) : 0u;
+        for (int i = 0; i < WORDS; i += 4) {
+          const uint4 u = reinterpret_cast<const uint4*>(piece)[i / 4];
+          w[i] = u.x;
+          w[i + 1] = u.y;
+          w[i + 2] = u.z;
+          w[i + 3] = u.w;
+        }
+      } else {
+        if (n > 0) off = 0;   // (lanes past the row's end keep the warp's)
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (i < n) {
+            if constexpr (sizeof(T) == 4) w[i] = bits(p[i]);
+            else w[i / 2] |= bits(p[i]) << (16 * (i & 1));
+          }
+        }
+      }
     } else if constexpr (AL == 2) {
       if (n > 0) {
 #pragma unroll
@@ -147,16 +198,28 @@ struct Raw16 {
     }
   }
   __device__ __forceinline__ void values(F2 (&v)[8]) const {
+    uint32_t t[PACKED];
+    if constexpr (AL == 0) {
+      shift_words<PACKED, sizeof(T)>(w, off, t);
+      if (left < 16) {
+#pragma unroll
+        for (int i = 0; i < PACKED; ++i) {
+          if constexpr (sizeof(T) == 4) t[i] = i < left ? t[i] : 0u;
+          else t[i] = 2 * i + 1 < left ? t[i] : 2 * i < left ? t[i] & 0xFFFFu : 0u;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PACKED; ++i) t[i] = w[i];
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float a, b;
       if constexpr (sizeof(T) == 4) {
-        a = __uint_as_float(w[2 * i]);
-        b = __uint_as_float(w[2 * i + 1]);
-      } else if constexpr (AL == 0) {
-        unpack2(w[2 * i] | (w[2 * i + 1] << 16), a, b, T());
+        a = __uint_as_float(t[2 * i]);
+        b = __uint_as_float(t[2 * i + 1]);
       } else {
-        unpack2(w[i], a, b, T());
+        unpack2(t[i], a, b, T());
       }
       v[i] = f2(a, b);
     }
@@ -168,51 +231,124 @@ struct Raw16 {
 };
 
 template <int AL, typename T>
-__device__ __forceinline__ void load16(const T* p, int n, F2 (&v)[8]) {
+__device__ __forceinline__ void load16(const T* p, int n, const void* begin, long long bytes, F2 (&v)[8]) {
   Raw16<AL, T> raw;
-  raw.load(p, n);
+  raw.load(p, n, begin, bytes);
   raw.values(v);
 }
 
-template <int AL, typename T>
-__device__ __forceinline__ void store16(T* p, int n, const F2 (&v)[8]) {
-  if constexpr (AL == 0) {
+// AL = 0: the 16 elements of SIZE bytes that each lane of a warp holds as W
+// words, n of which exist, to its place p (lanes 4 W bytes apart, full ones
+// first).  Piece j, the 16 bytes at p - off + 16 j, begins with the last `off`
+// bytes of the lane before (j = 0) or of the words before; a lane stores those
+// of its pieces that are whole.  The first lane's first piece lacks its start
+// and the last lane's last piece its end: they go in powers of two.  (One by
+// one, those elements were most of the instructions.)  The whole warp calls this.
+template <int W, int SIZE>
+__device__ __forceinline__ void store_unaligned(void* p, int n, const uint32_t (&w)[W]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+  const int bytes = (n < 0 ? 0 : n > 16 ? 16 : n) * SIZE;
+  const int next = __shfl_down_sync(0xFFFFFFFFu, bytes, 1);
+  uint8_t* piece = static_cast<uint8_t*>(p) - off;
+  uint32_t t[W + 8], c[W + 4];   // the last lane's end, this one's words, and their pieces
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) p[i] = from_f32<T>(i & 1 ? hi(v[i / 2]) : lo(v[i / 2]));
+  for (int i = 0; i < 4; ++i) {
+    t[i] = __shfl_up_sync(0xFFFFFFFFu, w[W - 4 + i], 1);
+    t[W + 4 + i] = 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) t[4 + i] = w[i];
+  if (off == 0) {
+#pragma unroll
+    for (int i = 0; i < W + 4; ++i) c[i] = t[4 + i];
   } else {
-    constexpr int WORDS = 4 * sizeof(T);
-    uint32_t w[WORDS];
+    shift_words<W + 4, SIZE>(t, 16 - off, c);
+  }
+  const bool cut = lane == 0 && off;   // piece 0 lacks its start
+  const int end = (int)off + bytes;    // bytes of the pieces that exist
+  if (cut && end < 16) {   // and its end
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (sizeof(T) == 2) {
-        w[i] = pack2<T>(lo(v[i]), hi(v[i]));
-      } else {
-        w[2 * i] = __float_as_uint(lo(v[i]));
-        w[2 * i + 1] = __float_as_uint(hi(v[i]));
+    for (int i = 0; i < 16 / SIZE; ++i) {
+      if (i * SIZE < bytes) {
+        if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + 4 * i) = w[i];
+        else if constexpr (SIZE == 2) *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p) + 2 * i) = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        else static_cast<uint8_t*>(p)[i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
       }
     }
-    if constexpr (AL == 2) {
-      if (n > 0) {
+  } else if (bytes > 0) {
 #pragma unroll
-        for (int i = 0; i < WORDS; i += 8) st32(reinterpret_cast<uint32_t*>(p) + i, *reinterpret_cast<uint32_t(*)[8]>(w + i));
+    for (int j = 0; j < W / 4; ++j)
+      if (16 * (j + 1) <= end && !(j == 0 && cut))
+        *reinterpret_cast<uint4*>(piece + 16 * j) = make_uint4(c[4 * j], c[4 * j + 1], c[4 * j + 2], c[4 * j + 3]);
+    if (cut) {   // bytes off to 15, from their end on
+      const uint32_t h = 16 - off;
+      if (h & 8) *reinterpret_cast<uint2*>(piece + 8) = make_uint2(c[2], c[3]);
+      if (h & 4) *reinterpret_cast<uint32_t*>(piece + (h & 8 ? 4 : 12)) = h & 8 ? c[1] : c[3];
+      if constexpr (SIZE < 4) {
+        const uint32_t v = off < 8 ? (off < 4 ? c[0] : c[1]) : (off < 12 ? c[2] : c[3]);   // the word that holds byte off
+        if (h & 2) *reinterpret_cast<uint16_t*>(piece + (off & 12) + 2) = (uint16_t)(v >> 16);
+        if (SIZE == 1 && (h & 1)) piece[off] = (uint8_t)(v >> (8 * (off & 3)));
       }
-    } else {
+    }
+    if (lane == 31 || next == 0) {   // bytes 0 to end % 16 - 1 of the last piece
+      const int j = end >> 4, e = end & 15;
+      uint32_t q[4] = {c[W], c[W + 1], c[W + 2], c[W + 3]};
+      if (j < W / 4) {   // (the row's end)
 #pragma unroll
-      for (int i = 0; i < WORDS; i += 4)
-        if (i < WORDS / 2 ? n > 0 : n > 8) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        for (int k = 0; k < W / 4; ++k) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[i] = j == k ? c[4 * k + i] : q[i];
+        }
+      }
+      uint8_t* last = piece + 16 * j;
+      if (e & 8) *reinterpret_cast<uint2*>(last) = make_uint2(q[0], q[1]);
+      if (e & 4) *reinterpret_cast<uint32_t*>(last + (e & 8)) = e & 8 ? q[2] : q[0];
+      if constexpr (SIZE < 4) {
+        const uint32_t v = e & 8 ? (e & 4 ? q[3] : q[2]) : (e & 4 ? q[1] : q[0]);   // the word behind
+        if (e & 2) *reinterpret_cast<uint16_t*>(last + (e & 12)) = (uint16_t)v;
+        if (SIZE == 1 && (e & 1)) last[e - 1] = (uint8_t)(v >> (8 * (e & 2)));
+      }
     }
   }
 }
 
+template <int AL, typename T>
+__device__ __forceinline__ void store16(T* p, int n, const F2 (&v)[8]) {
+  constexpr int WORDS = 4 * sizeof(T);
+  uint32_t w[WORDS];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      w[i] = pack2<T>(lo(v[i]), hi(v[i]));
+    } else {
+      w[2 * i] = __float_as_uint(lo(v[i]));
+      w[2 * i + 1] = __float_as_uint(hi(v[i]));
+    }
+  }
+  if constexpr (AL == 0) {
+    store_unaligned<WORDS, sizeof(T)>(p, n, w);
+  } else if constexpr (AL == 2) {
+    if (n > 0) {
+#pragma unroll
+      for (int i = 0; i < WORDS; i += 8) st32(reinterpret_cast<uint32_t*>(p) + i, *reinterpret_cast<uint32_t(*)[8]>(w + i));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4)
+      if (i < WORDS / 2 ? n > 0 : n > 8) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+}
+
+// 16 elements of the weight [K] from `at` on
 template <int AL>
-__device__ __forceinline__ void load16_typed(const void* p, int type, long long at, int n, F2 (&v)[8]) {
+__device__ __forceinline__ void load_weight(const void* p, int type, int K, int at, F2 (&v)[8]) {
   if (type == ROW_BF16)
-    load16<AL>(static_cast<const __nv_bfloat16*>(p) + at, n, v);
+    load16<AL>(static_cast<const __nv_bfloat16*>(p) + at, K - at, p, 2ll * K, v);
   else if (type == ROW_FP16)
-    load16<AL>(static_cast<const __half*>(p) + at, n, v);
+    load16<AL>(static_cast<const __half*>(p) + at, K - at, p, 2ll * K, v);
   else
-    load16<AL>(static_cast<const float*>(p) + at, n, v);
+    load16<AL>(static_cast<const float*>(p) + at, K - at, p, 4ll * K, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -328,9 +464,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, uint4 c) {
     if (n > 8) *reinterpret_cast<uint2*>(p + 8) = make_uint2(c.z, c.w);
   } else {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+    store_unaligned<4, 1>(p, n, w);
   }
 }
 
@@ -343,10 +477,8 @@ __device__ __forceinline__ void emit16(const RowArgs& a, int row, int vec, int n
   if constexpr (OUT == OUT_BLOCK) {
     float s;
     const uint4 c = quantize_block(v, &s);
-    if (n > 0) {
-      if ((vec & 7) == 0) a.scales[(long long)row * ((a.K + QBLOCK - 1) / QBLOCK) + (vec >> 3)] = s;
-      store_codes<AL>(static_cast<uint8_t*>(a.out) + at, n, c);
-    }
+    if (n > 0 && (vec & 7) == 0) a.scales[(long long)row * ((a.K + QBLOCK - 1) / QBLOCK) + (vec >> 3)] = s;
+    store_codes<AL>(static_cast<uint8_t*>(a.out) + at, n, c);
   } else if constexpr (OUT == OUT_STATIC) {
     uint32_t w[4];
 #pragma unroll
@@ -374,7 +506,9 @@ __device__ __forceinline__ void emit16(const RowArgs& a, int row, int vec, int n
 // goes on to the next rows with their loads already under way and the weight
 // kept in registers.  NV = 0 reads the row twice, for rows that do not fit.
 // residual_out may be the residual or x itself: every element is read by the
-// thread that writes it, before it is written.
+// warp that writes it, before it is written (store_unaligned writes a lane's
+// last elements from the next lane, after both have theirs; what else a piece
+// of load() covers is not used).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
@@ -392,9 +526,14 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 
 // MT: most threads a CTA has.  The registers are bounded for three CTAs of 256
 // threads an SM (16384 x 4096 in 16 bits: 72.6 us, with two 79.3, with four 83.7).
+// Rows that start anywhere (AL = 0) are bound by the instructions that shift
+// them into place and by what is in flight: there the next row is not loaded
+// ahead, which leaves registers for 768 threads an SM (8192 x 4099 in bf16:
+// 88 us, loaded ahead 119; in fp32 116 and 124).
 template <typename T, int NV, int OUT, int AL, int MT>
-__global__ void __launch_bounds__(MT, MT == 256 && NV == 1 && sizeof(T) == 2 ? 3 : 1) rmsnorm_kernel(const RowArgs a) {
-  __shared__ float part[2][16];   // in turn, so that one barrier a row will do
+__global__ void __launch_bounds__(MT, AL == 0 ? (MT < 768 ? 768 / MT : 1) : MT == 256 && NV == 1 && sizeof(T) == 2 ? 3 : 1) rmsnorm_kernel(const RowArgs a) {
+  constexpr bool AHEAD = AL > 0;
+  __shared__ float part[2][32];   // in turn, so that one barrier a row will do
   pdl_launch_dependents();
   pdl_wait();   // x, the residual and the weight may be the previous grid's output
   const int K = a.K;
@@ -411,18 +550,18 @@ __global__ void __launch_bounds__(MT, MT == 256 && NV == 1 && sizeof(T) == 2 ? 3
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int vec = threadIdx.x + i * blockDim.x, n = count(row, i);
-        cx[i].load(x + row * a.ldx + vec * 16, n);
-        if (res) cr[i].load(res + row * K + vec * 16, n);
+        cx[i].load(x + row * a.ldx + vec * 16, n, x, a.x_bytes);
+        if (res) cr[i].load(res + row * K + vec * 16, n, res, a.row_bytes);
       }
     };
     long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-    fetch(row);
+    if constexpr (AHEAD) fetch(row);
     F2 w[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int vec = threadIdx.x + i * blockDim.x;
       if (a.w) {
-        load16_typed<AL>(a.w, a.w_type, vec * 16, K - vec * 16, w[i]);
+        load_weight<AL>(a.w, a.w_type, K, vec * 16, w[i]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[i][j] = f2(1.f, 1.f);
@@ -432,6 +571,7 @@ __global__ void __launch_bounds__(MT, MT == 256 && NV == 1 && sizeof(T) == 2 ? 3
     // (the bound is of the CTA's first row: its threads meet in row_sum)
     for (long long first = (long long)blockIdx.x * blockDim.y; first < a.M; first += step, row += step, turn ^= 1) {
       F2 r[NV][8];
+      if constexpr (!AHEAD) fetch(row);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         cx[i].values(r[i]);
@@ -442,7 +582,7 @@ __global__ void __launch_bounds__(MT, MT == 256 && NV == 1 && sizeof(T) == 2 ? 3
           for (int j = 0; j < 8; ++j) r[i][j] = add2(r[i][j], b[j]);
         }
       }
-      if (first + step < a.M) fetch(row + step);
+      if (AHEAD && first + step < a.M) fetch(row + step);
       F2 sum = f2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -465,10 +605,10 @@ __global__ void __launch_bounds__(MT, MT == 256 && NV == 1 && sizeof(T) == 2 ? 3
       const long long row = first + threadIdx.y;
       const bool live = row < a.M;
       const auto load = [&](int vec, int n, F2 (&r)[8]) {
-        load16<AL>(x + row * a.ldx + vec * 16, n, r);
+        load16<AL>(x + row * a.ldx + vec * 16, n, x, a.x_bytes, r);
         if (res) {
           F2 b[8];
-          load16<AL>(res + row * K + vec * 16, n, b);
+          load16<AL>(res + row * K + vec * 16, n, res, a.row_bytes, b);
 #pragma unroll
           for (int j = 0; j < 8; ++j) r[j] = add2(r[j], b[j]);
         }
@@ -489,7 +629,7 @@ __global__ void __launch_bounds__(MT, MT == 256 && NV == 1 && sizeof(T) == 2 ? 3
         if (res) store16<AL>(res_out + row * K + vec * 16, n, r);
         F2 w[8];
         if (a.w) {
-          load16_typed<AL>(a.w, a.w_type, vec * 16, n, w);
+          load_weight<AL>(a.w, a.w_type, K, vec * 16, w);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[j] = f2(1.f, 1.f);
@@ -540,8 +680,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowArgs a, int parts) {
   const auto fetch = [&] {
     if (row < a.M) {
       const int at = (part * 32 + lane) * 16, n = a.K - at;
-      g.load(x + row * a.ldx + at, n);
-      if constexpr (GATE) u.load(x + row * a.ldx + a.K + at, n);
+      g.load(x + row * a.ldx + at, n, x, a.x_bytes);
+      if constexpr (GATE) u.load(x + row * a.ldx + a.K + at, n, x, a.x_bytes);
     }
   };
   fetch();

@@ -52,7 +52,7 @@ int sm_count() {
 // CTAs of a kernel that are resident at once, on all multiprocessors: what a
 // launch over many rows starts, since each goes on to the next rows itself
 template <typename K>
-long long resident_ctas(K kern, int threads, int (&cache)[17]) {
+long long resident_ctas(K kern, int threads, int (&cache)[33]) {
   int& n = cache[threads / 32];   // (every thread would write the same value)
   if (n == 0) {
     int v = 0;
@@ -78,7 +78,7 @@ dqgemm_status launch_rows(void (*kern)(KArgs...), dim3 grid, dim3 block, void* s
 
 template <typename T, int NV, int OUT, int AL, int MT>
 dqgemm_status norm_grid(const RowArgs& a, long long need, dim3 block, void* stream) {
-  static int cache[17] = {};
+  static int cache[33] = {};
   const long long most = resident_ctas(rmsnorm_kernel<T, NV, OUT, AL, MT>, (int)(block.x * block.y), cache);
   return launch_rows(rmsnorm_kernel<T, NV, OUT, AL, MT>, dim3((unsigned)std::min(need, most)), block, stream, a);
 }
@@ -87,15 +87,23 @@ template <typename T, int OUT, int AL>
 dqgemm_status norm_launch(const RowArgs& a, void* stream) {
   // threads a row: one vector each up to 512 of them (K = 8192: 82.8 us for
   // 8192 rows, with two each on half the threads 88.0), then two; rows past
-  // K = 16384 are read twice
-  const int vecs = (a.K + 15) / 16, per = vecs <= 512 ? 1 : 2;
-  const int tpr = std::min(512, ((vecs + per - 1) / per + 31) / 32 * 32);
+  // K = 16384 are read twice.  Rows that start anywhere: one each up to 1024
+  // (4096 x 12001 in bf16: 116 us, with two each 158).
+  constexpr int single = AL == 0 ? 1024 : 512;
+  const int vecs = (a.K + 15) / 16, per = vecs <= single ? 1 : 2;
+  const int tpr = std::min(single, ((vecs + per - 1) / per + 31) / 32 * 32);
   const int rows = std::max(1, 128 / tpr);
   const dim3 block(tpr, rows);
   const long long need = (a.M + (long long)rows - 1) / rows;
-  if (per == 1)
-    return tpr <= 256 ? norm_grid<T, 1, OUT, AL, 256>(a, need, block, stream) : norm_grid<T, 1, OUT, AL, 512>(a, need, block, stream);
-  return vecs <= 1024 ? norm_grid<T, 2, OUT, AL, 512>(a, need, block, stream) : norm_grid<T, 0, OUT, AL, 512>(a, need, block, stream);
+  if (vecs > 1024) return norm_grid<T, 0, OUT, AL, single>(a, need, block, stream);
+  if (tpr <= 256 && per == 1) return norm_grid<T, 1, OUT, AL, 256>(a, need, block, stream);
+  if constexpr (AL == 0) {
+    return tpr <= 384   ? norm_grid<T, 1, OUT, AL, 384>(a, need, block, stream)
+           : tpr <= 768 ? norm_grid<T, 1, OUT, AL, 768>(a, need, block, stream)
+                        : norm_grid<T, 1, OUT, AL, 1024>(a, need, block, stream);
+  } else {
+    return per == 1 ? norm_grid<T, 1, OUT, AL, 512>(a, need, block, stream) : norm_grid<T, 2, OUT, AL, 512>(a, need, block, stream);
+  }
 }
 
 template <typename T, bool GATE, int OUT, int AL>
@@ -104,7 +112,7 @@ dqgemm_status plain_launch(const RowArgs& a, void* stream) {
   const long long items = (long long)parts * a.M;
   // (few warps: one a CTA, so that they spread over the multiprocessors)
   const int per = (int)std::max<long long>(1, std::min<long long>(8, items / sm_count()));
-  static int cache[17] = {};
+  static int cache[33] = {};
   const int ctas = (int)std::min((items + per - 1) / per, resident_ctas(rows_kernel<T, GATE, OUT, AL>, 32 * per, cache));
   return launch_rows(rows_kernel<T, GATE, OUT, AL>, dim3(ctas), dim3(32 * per), stream, a, parts);
 }
@@ -143,6 +151,9 @@ dqgemm_status run_rows(RowArgs& a, int type, int out, float s_out, void* stream)
   int al = 0;
   const dqgemm_status st = check_rows(a, type, out, OP == 1 ? 2 : 1, &al);
   if (st != DQ_OK) return st;
+  const long long tb = (long long)type_bytes(type);
+  a.x_bytes = ((a.M - 1) * a.ldx + (OP == 1 ? 2 : 1) * (long long)a.K) * tb;
+  a.row_bytes = (long long)a.M * a.K * tb;
   volatile float one = 1.f;
   volatile float r = one / a.s_out;   // an fp32 division
   a.r_out = r;
