@@ -245,6 +245,32 @@ def test_special_values(K):
     assert (y[0] == 0).all() and torch.isnan(y[1]).all() and torch.isnan(y[2, 3]) and torch.isfinite(y[3:5]).all()
 
 
+@pytest.mark.parametrize("op,dt", [("norm", "bf16"), ("norm", "fp32"), ("gate", "bf16"), ("gate", "fp32")])
+def test_few_codes_differ_from_the_exact_ones(op, dt):
+    """A value whose error is d of it changes its code where a border between
+    two codes lies in between: for one of |q| / step d <= 16 d of the values.
+    With u = 2^-24, d is for the norm half of the sum's (8 + 6 + 8) u and of the
+    mean's 2 u, the root's 4 u, two products' 2 u and the quotient's u: 19 u in
+    all.  For the gate with g > 0: the exponential's (4 u + 1.45 u g) e^-g /
+    (1 + e^-g) <= 2.1 u, the sum 1 + e^-g u, its reciprocal 2 u, two products
+    2 u, the quotient u: 8.1 u."""
+    M, K, s = 2048, 4096, 0.013
+    x = gen((M, K if op == "norm" else 2 * K), 5, dt)
+    if op == "norm":
+        w = gen((K,), 6, dt)
+        q = dq.rmsnorm(x, w, quant="fp8_static", s_out=s)
+        r = x.double()
+        ref, d = r * torch.rsqrt(r.square().mean(1, keepdim=True) + 1e-6) * w.double(), 19 * U
+    else:
+        x[:, :K] = x[:, :K].abs()
+        q = dq.silu_mul(x, quant="fp8_static", s_out=s)
+        g, u = x.double().chunk(2, 1)
+        ref, d = g * torch.sigmoid(g) * u, 8.1 * U
+    exact = (ref / float(np.float32(s))).float().clamp(-448, 448).to(torch.float8_e4m3fn)
+    other = (q.view(torch.float8_e4m3fn).float() != exact.float()).sum().item()
+    assert other <= 16 * d * M * K, other
+
+
 def test_empty_batch():
     x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
     q, s = dq.quantize_act_fp8_block(x)
