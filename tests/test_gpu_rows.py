@@ -289,6 +289,20 @@ def test_offsets_past_32_bits():
     assert torch.equal(n[-3:], dq.rmsnorm(x[-3:].contiguous()))
 
 
+def test_offsets_past_32_bits_of_rows_that_start_anywhere():
+    M, K = 70000, 32771
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = gen((3, K), 16, "bf16")
+    last = x[-3:].clone()
+    q, s = dq.quantize_act_fp8_block(x)
+    q2, s2 = dq.quantize_act_fp8_block(last)
+    assert torch.equal(q[-3:], q2) and torch.equal(s[-3:], s2) and not q[:-3].any()
+    del q, s
+    n, r = dq.rmsnorm(x, residual=x, residual_out=x)          # r = 2 x, in place
+    n2, r2 = dq.rmsnorm(last, residual=last)
+    assert torch.equal(n[-3:], n2) and torch.equal(x[-3:], r2) and not n[:-3].any() and not x[:-3].any()
+
+
 def test_streams_and_graphs():
     x, r = gen((64, 4096), 17, "bf16"), gen((64, 4096), 18, "bf16")
     ref = dq.rmsnorm(x, residual=r, quant="fp8_block")
