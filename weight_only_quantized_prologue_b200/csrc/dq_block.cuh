@@ -742,8 +742,96 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// Between the two CTAs.  `addr`: a barrier of either, as the cluster addresses
+// it.  An arrival orders nothing by itself (relaxed), and need not:
+//  - on acc_empty it follows tcgen05.wait::ld and tcgen05.fence::before_thread_sync,
+//    and the MMA thread's wait is followed by tcgen05.fence::after_thread_sync:
+//    the pair of fences orders tensor memory across any wait of their scope;
+//  - on full it only announces bytes.  What the MMAs read is published by the
+//    copies themselves, whose completion on the barrier is a release at cluster
+//    scope, and the MMA thread's wait there acquires at cluster scope.
+// (With a release on every arrival of the epilogue the large product took 1187 us, not 888.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes)
+               : "memory");
+}
+// a tile into this CTA's shared memory, its bytes counted on a barrier of either CTA
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Waits on barriers that the other CTA completes: their scope is the cluster.
+// ACQUIRE false: for tensor memory, with a tcgen05 fence behind the wait.
+template <bool ACQUIRE>
+__device__ __forceinline__ bool mbar_try_wait_pair(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (ACQUIRE)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  return ok != 0;
+}
+// as block_wait
+template <bool ACQUIRE>
+__device__ __forceinline__ bool block_wait_pair(uint64_t* bar, uint32_t parity, const WaitCtl ctl) {
+  if (mbar_try_wait_pair<ACQUIRE>(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (int round = 0;; ++round) {
+    if (round > 0 || ctl.timeout_ns < 1000u) {
+      if (t0 == 0) t0 = globaltimer_ns();
+      if (wait_give_up(ctl, t0)) return false;
+    }
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_pair<ACQUIRE>(bar, parity)) return true;
+  }
+}
+// as block_wait_warp, for tensor memory
+__device__ __forceinline__ bool block_wait_warp_pair(uint64_t* bar, uint32_t parity, const WaitCtl ctl) {
+  uint64_t t0 = 0;
+  for (int i = ctl.timeout_ns < 1000u ? 63 : 0;; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait_pair<false>(bar, parity))) return true;
+    if ((i & 63) == 63) {
+      if (t0 == 0) t0 = globaltimer_ns();
+      if (__any_sync(0xFFFFFFFFu, wait_give_up(ctl, t0))) return false;
+    }
+  }
+}
+// the stage's copies have landed and the buffer has been read, looked at together
+__device__ __forceinline__ bool pair_ready(uint64_t* full, uint32_t pf, uint64_t* acc_empty, uint32_t pe) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(full)), "r"(pf), "r"(smem_u32(acc_empty)), "r"(pe)
+      : "memory");
+  return ok != 0;
 }
 
 // shared -> global, complete in the issuing thread's bulk group
@@ -757,12 +845,12 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// a look at a barrier whose answer is used later
+// a look at a barrier whose answer is used later (as mbar_try_wait_pair<false>)
 __device__ __forceinline__ uint32_t mbar_peek(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -802,15 +890,18 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ uint8_t smem_raw[];
   // (the same offset in both CTAs: the dynamic base is the same)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);   // this CTA's copies of a stage have landed
-  uint64_t* peer_full = full + C::ST;        // leader: the other CTA's have
-  uint64_t* empty = peer_full + C::ST;       // both: the pair's MMAs have read the stage
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);   // leader: both CTAs' copies of a stage have landed
+  uint64_t* empty = full + C::ST;            // both: the pair's MMAs have read the stage
   uint64_t* acc_full = empty + C::ST;        // both
   uint64_t* acc_empty = acc_full + 2 * C::PB;    // leader: the 8 + 8 epilogue warps have read a buffer
-  uint64_t* drain = acc_empty + 2 * C::PB;
+  uint64_t* drain = acc_empty + 2 * C::PB;       // both: every MMA of a half is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((3 * C::ST + 4 * C::PB + 2) * 8 + 8 <= C::BAR_BYTES, "barriers");
+  // how this CTA ended, and how the other did: stages filled << 3 | MMAs issued in half h << (1 + h) | a wait gave up
+  volatile uint32_t* ended = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);
+  volatile uint32_t* other_ended = reinterpret_cast<volatile uint32_t*>(tmem_slot + 3);
+  volatile uint32_t* issued_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 4);   // [2]
+  static_assert((2 * C::ST + 4 * C::PB + 2) * 8 + 24 <= C::BAR_BYTES, "barriers");
   int* start = reinterpret_cast<int*>(smem + C::TAB_OFF);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -820,8 +911,7 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&peer_full[s], 1);
+      mbar_init(&full[s], 2);   // each CTA announces its own bytes
       mbar_init(&empty[s], 2);
     }
     for (int b = 0; b < 2 * C::PB; ++b) {
@@ -831,6 +921,8 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
     mbar_init(drain, 1);
     mbar_init(drain + 1, 1);
     *abort_flag = 0;
+    *ended = 0;
+    issued_flag[0] = issued_flag[1] = 0;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
@@ -857,34 +949,26 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
       // ---------------------------------------------------------- copies
       if (elect_one()) {
         if constexpr (!GROUPED) pdl_wait();
+        const uint32_t full_addr = dsmem_addr(full, 0);
         int it = 0, s = 0;
         uint32_t ph = 0;
         bool ok = true;
         for (int t = t0; ok && t < tiles; t += step) {
           const BlockTile tl = block_tile<256, 256, GROUPED>(p, start, t);
           for (int b = 0; b < p.kb; ++b, ++it) {
-            if (it >= C::ST && !block_wait(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
-            mbar_arrive_expect_tx(&full[s], C::STAGE);
-            tma_load_2d(smem + s * C::STAGE, &tmap_x, b * 128, tl.m0 + rank * 128, &full[s]);
-            tma_load_2d(smem + s * C::STAGE + C::A_BYTES, &tmap_w, b * 128, tl.e * p.N + tl.n0 + rank * 64, &full[s]);
-            tma_load_2d(smem + s * C::STAGE + C::A_BYTES + 8192, &tmap_w, b * 128, tl.e * p.N + tl.n0 + 128 + rank * 64, &full[s]);
+            if (it >= C::ST && !block_wait_pair<true>(&empty[s], ph ^ 1, ctl())) { ok = false; break; }
+            const uint32_t bar = full_addr + s * 8;
+            mbar_arrive_expect_tx_cluster(bar, C::STAGE);
+            tma_load_2d_pair(smem + s * C::STAGE, &tmap_x, b * 128, tl.m0 + rank * 128, bar);
+            tma_load_2d_pair(smem + s * C::STAGE + C::A_BYTES, &tmap_w, b * 128, tl.e * p.N + tl.n0 + rank * 64, bar);
+            tma_load_2d_pair(smem + s * C::STAGE + C::A_BYTES + 8192, &tmap_w, b * 128, tl.e * p.N + tl.n0 + 128 + rank * 64, bar);
             if (++s == C::ST) { s = 0; ph ^= 1; }
           }
         }
-        for (int i = it > C::ST ? it - C::ST : 0; i < it; ++i) block_wait(&full[i % C::ST], (i / C::ST) & 1, ctl_drain());
-      }
-    } else if (warp == 2 && rank == 1) {
-      // ---------------------------------------------------------- tell the leader that this CTA's half has landed
-      if (elect_one()) {
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int t = t0; ok && t < tiles; t += step)
-          for (int b = 0; b < p.kb; ++b) {
-            if (!block_wait(&full[s], ph, ctl())) { ok = false; break; }
-            mbar_arrive_cluster(dsmem_addr(&peer_full[s], 0));
-            if (++s == C::ST) { s = 0; ph ^= 1; }
-          }
+        *ended = (uint32_t)it << 3;
+        // the leader's last signals have arrived before this CTA can leave
+        for (int i = it > C::ST ? it - C::ST : 0; ok && i < it; ++i)
+          ok = block_wait_pair<true>(&empty[i % C::ST], (i / C::ST) & 1, ctl());
       }
     } else if ((warp == 1 || warp == 3) && rank == 0) {
       // ---------------------------------------------------------- MMA
@@ -895,10 +979,10 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
         bool ok = true, issued = false;
         for (int t = t0; ok && t < tiles; t += step) {
           for (int b = 0; b < p.kb; ++b) {
-            // (one after the other the three looks cost three latencies)
-            if (!mbar_try_wait3(&full[s], ph, &peer_full[s], ph, &acc_empty[h * 2 + pb], pph ^ 1) &&
-                (!block_wait(&full[s], ph, ctl()) || !block_wait(&peer_full[s], ph, ctl()) ||
-                 !block_wait(&acc_empty[h * 2 + pb], pph ^ 1, ctl()))) { ok = false; break; }
+            // (one after the other the two looks cost two latencies)
+            if (!pair_ready(&full[s], ph, &acc_empty[h * 2 + pb], pph ^ 1) &&
+                (!block_wait_pair<true>(&full[s], ph, ctl()) ||
+                 !block_wait_pair<false>(&acc_empty[h * 2 + pb], pph ^ 1, ctl()))) { ok = false; break; }
             tc_fence_after();
             const uint32_t ab = smem_u32(smem + s * C::STAGE), bb = ab + C::A_BYTES + h * 8192;
 #pragma unroll
@@ -912,8 +996,8 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
           }
         }
         if (issued) {
-          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain + h))
-                       : "memory");
+          issued_flag[h] = 1u;
+          tc_commit_pair(drain + h);
           block_wait(drain + h, 0, ctl_drain());
         }
       }
@@ -953,7 +1037,7 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
           if (live) nx = sxr[b + 1];
           if (live_n) nw = sw[b + 1];
         }
-        if (!__all_sync(0xFFFFFFFFu, ready) && !block_wait_warp(&acc_full[h * 2 + pb], pph, ctl())) { ok = false; break; }
+        if (!__all_sync(0xFFFFFFFFu, ready) && !block_wait_warp_pair(&acc_full[h * 2 + pb], pph, ctl())) { ok = false; break; }
         tc_fence_after();
         const uint32_t ta = tmem + lane_base + pb * 256 + h * 128;
         uint64_t* next_bar = &acc_full[h * 2 + (pb ^ 1)];
@@ -1022,8 +1106,36 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t e = *ended | issued_flag[0] << 1 | issued_flag[1] << 2 | (*abort_flag ? 1u : 0u);
+    *ended = e;
+    st_dsmem_u32(dsmem_addr(const_cast<uint32_t*>(other_ended), rank ^ 1), e);
+  }
+  __syncwarp();
   // both CTAs are done with each other's barriers, shared and tensor memory
+  // (where no wait gave up: every copy was waited for by an MMA, every MMA by
+  // an epilogue warp)
   cluster_sync();
+  const uint32_t mine = *ended, other = *other_ended;
+  if ((mine | other) & 1u) {
+    // A wait gave up.  Copies and MMAs of either CTA may still run: they end
+    // before this CTA's shared memory is given back.  A CTA has filled at
+    // most ST stages more than the other; for those the other arrives too, with
+    // no bytes, so that each phase the leader waits for here completes.
+    if (warp == 0 && elect_one()) {
+      const int a = (int)(mine >> 3), b = (int)(other >> 3), last = max(a, b);
+      for (int i = a; i < b; ++i) mbar_arrive_cluster(dsmem_addr(full, 0) + (i % C::ST) * 8);
+      if (rank == 0) {
+        for (int i = last > C::ST ? last - C::ST : 0; i < last; ++i)
+          block_wait_pair<true>(&full[i % C::ST], (i / C::ST) & 1, ctl_drain());
+      } else {
+        for (int h = 0; h < 2; ++h)
+          if (other >> (1 + h) & 1u) block_wait_pair<true>(drain + h, 0, ctl_drain());
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   tc_fence_after();
   if (warp == 0) tmem_dealloc_pair(tmem, C::TMEM_COLS);
 }
