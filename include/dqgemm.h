@@ -370,7 +370,8 @@ dqgemm_status dqgemm_pack_host(dqgemm_format fmt, const float* W, int K, int N,
 /* Same as dqgemm_pack_host on the GPU: W, packed and scales are device
  * pointers; results are bit-identical to dqgemm_pack_host.  If
  * `global_scale` (host pointer) is not NULL the call synchronizes `stream`
- * and stores g there.  Allocates and frees 8 bytes of device memory. */
+ * and stores g there.  Allocates and frees 8 bytes of device memory.  The
+ * buffers are 16-byte aligned (DQ_FP8_BLOCK128: scales 4-byte aligned). */
 dqgemm_status dqgemm_pack_device(dqgemm_format fmt, const float* W, int K, int N,
                                  void* packed, void* scales, float* global_scale,
                                  void* stream);

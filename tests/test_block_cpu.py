@@ -61,3 +61,13 @@ def test_storage_shapes():
     import numpy as np
 
     assert dq.storage_shapes("fp8_block", 272, 130) == ((130, 272), np.uint8, (2, 3), np.float32)
+
+
+def test_packers_take_scales_that_begin_at_any_fp32():
+    # an expert's scales lie N / 128 * K / 128 values behind the one's before it
+    lib, f = dq._native.lib(), dq.FORMATS["fp8_block"]
+    for entry in (lib.dqgemm_pack_device, lib.dqgemm_pack_device_noalloc):
+        assert entry(f, 16, 128, 128, 16, 18, None, None) == ALIGN
+        assert entry(f, 20, 128, 128, 16, 16, None, None) == ALIGN
+        assert entry(f, 16, 128, 128, 20, 16, None, None) == ALIGN
+        assert entry(dq.FORMATS["fp8"], 16, 128, 128, 16, 20, None, None) == ALIGN

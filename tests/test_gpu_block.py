@@ -475,3 +475,22 @@ def test_quantize_replaces_linears_by_block_scaled_ones():
     with torch.no_grad():
         y = model(x)
     assert torch.equal(y, l2(torch.relu(l1(x.view(-1, 256)))).view(3, 7, 64))
+
+
+@pytest.mark.parametrize("E,N,K", [(3, 128, 128), (3, 384, 128), (4, 384, 1152), (5, 200, 336), (3, 1, 16), (2, 256, 256)])
+def test_experts_from_float_at_any_count_of_blocks(E, N, K):
+    w = (randn((E, N, K), 161) * 0.1).float()
+    ex = dq.QuantizedExperts.from_float("fp8_block", w.cuda())
+    d = ex.dequantize().double().cpu().numpy()
+    for e in range(E):
+        q, s = B.quantize_weight(w[e].double().numpy())
+        wide = np.repeat(np.repeat(s.astype(np.float64), 128, 0), 128, 1)[:N, :K]
+        assert np.array_equal(d[e], F.bf16((F.e4m3_decode(q) * wide).astype(np.float32)))
+    M = 2 * E
+    x, xq, xs = rows(M, K, 163)
+    y = ex(x.cuda(), torch.arange(0, M + 1, 2, dtype=torch.int32, device="cuda"))
+    for e in range(E):
+        q, s = B.quantize_weight(w[e].double().numpy())
+        a, z = 2 * e, 2 * e + 2
+        ref = B.linear(xq[a:z], xs[a:z], q, s)
+        check(y[a:z], ref, bound(xq[a:z], xs[a:z], q, s, ref))

@@ -43,6 +43,12 @@ size_t scale_bytes(int fmt, int K, int N) {
   }
 }
 
+// what the GPU packers need of `scales`: the block-scaled one writes single fp32
+// values (an expert's scales begin anywhere in [E, N / 128, K / 128])
+bool packed_scales_aligned(int fmt, const void* p) {
+  return fmt == FMT_FP8B ? reinterpret_cast<uintptr_t>(p) % sizeof(float) == 0 : aligned16(p);
+}
+
 dqgemm_status check_shape(int fmt, int K, int N) {
   if (fmt < 0 || (fmt > FMT_W4A4NV && fmt != FMT_FP8B) || K <= 0 || N <= 0) return DQ_ERR_INVALID_ARG;
   switch (storage_fmt(fmt)) {
@@ -1022,7 +1028,7 @@ dqgemm_status dqgemm_pack_device(dqgemm_format fmt_, const float* W, int K, int 
   dqgemm_status st = check_shape(fmt, K, N);
   if (st != DQ_OK) return st;
   if (!W || !packed || !scales) return DQ_ERR_INVALID_ARG;
-  if (!aligned16(W) || !aligned16(packed) || !aligned16(scales)) return DQ_ERR_ALIGNMENT;
+  if (!aligned16(W) || !aligned16(packed) || !packed_scales_aligned(fmt, scales)) return DQ_ERR_ALIGNMENT;
   if (fmt == FMT_FP8B) {
     st = block_pack_device(W, K, N, packed, scales, static_cast<cudaStream_t>(stream));
     if (st == DQ_OK && global_scale) {
@@ -1101,7 +1107,7 @@ dqgemm_status dqgemm_pack_device_noalloc(dqgemm_format fmt_, const float* W, int
   dqgemm_status st = check_shape(fmt, K, N);
   if (st != DQ_OK) return st;
   if (!W || !packed || !scales) return DQ_ERR_INVALID_ARG;
-  if (!aligned16(W) || !aligned16(packed) || !aligned16(scales)) return DQ_ERR_ALIGNMENT;
+  if (!aligned16(W) || !aligned16(packed) || !packed_scales_aligned(fmt, scales)) return DQ_ERR_ALIGNMENT;
   if (fmt == FMT_FP8B) {
     st = block_pack_device(W, K, N, packed, scales, static_cast<cudaStream_t>(stream));
     if (st == DQ_OK && global_scale) {
