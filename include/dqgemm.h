@@ -338,7 +338,8 @@ dqgemm_status dqgemm_rmsnorm(dqgemm_dtype type, const void* x, long long ldx, co
                              dqgemm_out out_kind, float s_out, void* out, float* scales, void* stream);
 
 /* Gated SiLU: x [M, 2K] holds the gate g in its first K columns and u in the
- * others (ldx >= 2K);  v = g / (1 + exp(-g)) * u. */
+ * others (ldx >= 2K);  v = g / (1 + exp(-g)) * u, also where exp(-g) is beyond
+ * fp32 (g < -88.7) and a large u brings v back into it. */
 dqgemm_status dqgemm_silu_mul(dqgemm_dtype type, const void* x, long long ldx, int M, int K, dqgemm_out out_kind,
                               float s_out, void* out, float* scales, void* stream);
 

@@ -324,3 +324,35 @@ def test_streams_and_graphs():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
+@pytest.mark.parametrize("dt,odt", [("bf16", "bf16"), ("fp32", "fp32"), ("fp32", "bf16"), ("fp32", "fp16"), ("bf16", "fp32")])
+@pytest.mark.parametrize("K", [4096, 4100, 4099])
+def test_silu_mul_far_below_zero_with_large_factors(dt, odt, K):
+    """e^-g leaves fp32 at -88.7 and its reciprocal the normal numbers at -87.3; u
+    up to 3e38 makes ordinary numbers of the results down to g = -180.  The
+    tolerance is the gate's: e^(g/4) four times is within 4 x 2 units of 2^-23,
+    its products within 5 more halves."""
+    M = 6
+    g = torch.linspace(-205, -60, M * K, dtype=torch.float64).reshape(K, M).T
+    up = torch.exp2(torch.linspace(0, 95 if odt == "fp16" else 126, K)[torch.randperm(K, generator=torch.Generator().manual_seed(1))])
+    u = up * (1 - 2 * (torch.arange(M)[:, None] % 2)) * (1 + torch.rand((M, K), generator=torch.Generator().manual_seed(2)) / 2)
+    x = torch.cat([g, u.double()], 1).to(DT[dt]).cuda()
+    ref = B.silu_mul(f64(x))
+    rel = (8 + 1.2 * np.abs(f64(x)[:, :K])) * 2.0 ** -23
+    check_float(dq.silu_mul(x, out_dtype=DT[odt]), ref, odt, rel)
+    # a row of blocks by size, so that a block's scale is its own elements'
+    order = torch.arange(K) * 61 % K if K % 61 else torch.arange(K)
+    near = torch.cat([torch.linspace(-95, -85, K)[order].expand(M, K), torch.full((M, K), 2.0 ** 120)], 1).to(DT[dt]).cuda()
+    q, s = dq.silu_mul(near, quant="fp8_block")
+    check_codes(q, s, B.silu_mul(f64(near)), float((8 + 1.2 * 96) * 2.0 ** -23))
+    # an element does not depend on its neighbours
+    mixed = x.clone()
+    mixed[:, :K][:, 1::2] = 1.0
+    a, b = dq.silu_mul(x, out_dtype=DT[odt]), dq.silu_mul(mixed, out_dtype=DT[odt])
+    assert torch.equal(a[:, 0::2], b[:, 0::2])
+    x[:, :K] = x[:, :K].clamp(min=-79)
+    mixed = x.clone()
+    mixed[:, :K][:, 1::2] = -150.0
+    a, b = dq.silu_mul(x, out_dtype=DT[odt]), dq.silu_mul(mixed, out_dtype=DT[odt])
+    assert torch.equal(a[:, 0::2], b[:, 0::2])

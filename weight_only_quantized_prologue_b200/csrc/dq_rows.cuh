@@ -199,6 +199,11 @@ struct Raw16 {
   }
   __device__ __forceinline__ void values(F2 (&v)[8]) const {
     uint32_t t[PACKED];
+    words(t);
+    unpack(t, v);
+  }
+  // the vector's words, those that do not exist as 0 ...
+  __device__ __forceinline__ void words(uint32_t (&t)[PACKED]) const {
     if constexpr (AL == 0) {
       shift_words<PACKED, sizeof(T)>(w, off, t);
       if (left < 16) {
@@ -212,6 +217,9 @@ struct Raw16 {
 #pragma unroll
       for (int i = 0; i < PACKED; ++i) t[i] = w[i];
     }
+  }
+  // ... and as numbers
+  static __device__ __forceinline__ void unpack(const uint32_t (&t)[PACKED], F2 (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float a, b;
@@ -649,7 +657,10 @@ __global__ void __launch_bounds__(MT, AL == 0 ? (MT < 768 ? 768 / MT : 1) : MT =
 // ---------------------------------------------------------------------------
 // FAST (outputs of 16 or 8 bits): the hardware's exponential and reciprocal.
 // Their error, about 2^-22 plus 2^-24 per unit of |g|, stays far below half a
-// step of the output wherever the result is not itself vanishing.
+// step of the output.  For g down to GATE_TAIL: below -87.3 the reciprocal of
+// 1 + e^-g would be flushed to 0, below -88.7 e^-g overflows, while a large u
+// makes the result an ordinary number still.
+constexpr float GATE_TAIL = -80.f;
 template <bool FAST>
 __device__ __forceinline__ F2 silu_mul2(F2 g, F2 u) {
   if constexpr (FAST) {
@@ -665,9 +676,58 @@ __device__ __forceinline__ F2 silu_mul2(F2 g, F2 u) {
     return f2(lo(g) / (1.f + expf(-lo(g))) * lo(u), hi(g) / (1.f + expf(-hi(g))) * hi(u));
   }
 }
+// For g < GATE_TAIL 1 + e^-g is e^-g in fp32, so the result is g e^g u: taken in
+// four factors of e^(g/4), each of them (g > -349) and every partial product
+// that a result within fp32 has an ordinary number.  FAST: within 2^-20 plus
+// 2^-23 per unit of |g|.
+template <bool FAST>
+__device__ __forceinline__ float silu_mul_tail(float g, float u) {
+  float h;
+  if constexpr (FAST) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(g * (0.25f * 1.44269504f)));
+  else h = expf(0.25f * g);
+  return (g * h * h) * (u * h * h);
+}
+// Whether one of 16 packed elements may lie below GATE_TAIL, from their bits: as
+// unsigned numbers those of negative values grow with the magnitude (a NaN
+// with a sign counts too).  Three-way maxima of whole words: 6 instructions for
+// 16 elements in 16 bits, where minima of the numbers are 15 (8192 x 14336 to
+// static codes, bound by issue: 102 us, by minima 105; without this test 101).
+template <typename T, int N>
+__device__ __forceinline__ bool tail_among(const uint32_t (&t)[N]) {
+  uint32_t m = t[0];
+  if constexpr (sizeof(T) == 4) {
+    m = max(m, t[1]);
+#pragma unroll
+    for (int i = 2; i < N; i += 2) m = __vimax3_u32(m, t[i], t[i + 1]);
+    return m > 0xC2A00000u;
+  } else {
+    constexpr uint32_t limit = std::is_same<T, __half>::value ? 0xD500D500u : 0xC2A0C2A0u;   // -80 twice
+    m = __vimax3_u16x2(m, t[1], limit);
+#pragma unroll
+    for (int i = 2; i < N; i += 2) m = __vimax3_u16x2(m, t[i], t[i + 1]);
+    return m != limit;
+  }
+}
+// v = silu(v) * w of 16 elements; TAIL: some of them may be below GATE_TAIL.
+// What an element becomes does not depend on the others.
+template <bool FAST, bool TAIL>
+__device__ __forceinline__ void silu_mul16(F2 (&v)[8], const F2 (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const F2 y = silu_mul2<FAST>(v[i], w[i]);
+    if constexpr (TAIL)
+      v[i] = f2(lo(v[i]) < GATE_TAIL ? silu_mul_tail<FAST>(lo(v[i]), lo(w[i])) : lo(y),
+                hi(v[i]) < GATE_TAIL ? silu_mul_tail<FAST>(hi(v[i]), hi(w[i])) : hi(y));
+    else
+      v[i] = y;
+  }
+}
 
+// The gate's registers are bounded for three CTAs an SM, in static codes four
+// (102 us where three take 105; to bf16 three take 107 us and four 115): without
+// a bound the tail, which hardly any call reaches, sets their number.
 template <typename T, bool GATE, int OUT, int AL>
-__global__ void __launch_bounds__(256) rows_kernel(const RowArgs a, int parts) {
+__global__ void __launch_bounds__(256, !GATE || sizeof(T) == 4 || OUT == OUT_FP32 ? 1 : AL == 2 && OUT == OUT_STATIC ? 4 : 3) rows_kernel(const RowArgs a, int parts) {
   pdl_launch_dependents();
   pdl_wait();
   const T* x = static_cast<const T*>(a.x);
@@ -687,8 +747,16 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowArgs a, int parts) {
   fetch();
   while (row < a.M) {
     F2 v[8], w[8];
-    g.values(v);
-    if constexpr (GATE) u.values(w);
+    bool tail = false;
+    if constexpr (GATE) {
+      uint32_t t[Raw16<AL, T>::PACKED];
+      g.words(t);
+      tail = tail_among<T>(t);
+      Raw16<AL, T>::unpack(t, v);
+      u.values(w);
+    } else {
+      g.values(v);
+    }
     const long long r = row;
     const int vec = part * 32 + lane;
     row += dr;
@@ -698,9 +766,15 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowArgs a, int parts) {
       ++row;
     }
     fetch();
+    // (two ways out: where they meet before emit16 the compiler cannot mix the
+    // gate's instructions with the quantizer's, to static codes 113 us)
     if constexpr (GATE) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = silu_mul2<OUT != OUT_FP32>(v[i], w[i]);
+      if (__any_sync(0xFFFFFFFFu, tail)) {
+        silu_mul16<OUT != OUT_FP32, true>(v, w);
+        emit16<OUT, AL>(a, (int)r, vec, a.K - vec * 16, v);
+        continue;
+      }
+      silu_mul16<OUT != OUT_FP32, false>(v, w);
     }
     emit16<OUT, AL>(a, (int)r, vec, a.K - vec * 16, v);
   }
