@@ -356,3 +356,31 @@ def test_silu_mul_far_below_zero_with_large_factors(dt, odt, K):
     mixed[:, :K][:, 1::2] = -150.0
     a, b = dq.silu_mul(x, out_dtype=DT[odt]), dq.silu_mul(mixed, out_dtype=DT[odt])
     assert torch.equal(a[:, 0::2], b[:, 0::2])
+
+
+def test_gradients_raise_where_they_would_be_missing():
+    x, r, w = gen((4, 256), 31, "bf16"), gen((4, 256), 32, "bf16"), gen((256,), 33, "bf16")
+    ref = dq.rmsnorm(x, w, residual=r)
+    for which in (0, 1, 2):
+        a = [x.clone(), w.clone(), r.clone()]
+        a[which].requires_grad_(True)
+        y, r2 = dq.rmsnorm(a[0], a[1], residual=a[2])
+        assert torch.equal(y, ref[0]) and torch.equal(r2, ref[1])
+        with pytest.raises(RuntimeError, match="inference only"):
+            y.float().sum().backward()
+        q, s, r3 = dq.rmsnorm(a[0], a[1], residual=a[2], quant="fp8_block")
+        assert r3.requires_grad == (which != 1)        # the new residual has no weight in it
+        if which != 1:
+            with pytest.raises(RuntimeError, match="inference only"):
+                r3.float().sum().backward()
+    g = torch.cat([x, r], 1).requires_grad_(True)
+    with pytest.raises(RuntimeError, match="inference only"):
+        dq.silu_mul(g).float().sum().backward()
+    with torch.no_grad():
+        assert not dq.silu_mul(g).requires_grad and not dq.rmsnorm(x.clone().requires_grad_(True)).requires_grad
+    ex = dq.QuantizedExperts.from_float("fp8_block", torch.randn(2, 128, 256, device="cuda"))
+    off = torch.tensor([0, 1, 4], dtype=torch.int32, device="cuda")
+    y = ex(x.clone().requires_grad_(True), off)
+    assert torch.equal(y, ex(x, off))
+    with pytest.raises(RuntimeError, match="inference only"):
+        y.float().sum().backward()

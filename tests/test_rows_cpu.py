@@ -96,3 +96,16 @@ def test_output_arguments_are_refused():
         rows._outputs(x, 4, 256, None, None, torch.int8, None, None)
     with pytest.raises(ValueError, match="shape"):
         rows._outputs(x, 4, 256, "fp8_block", None, None, Fake(torch.zeros(4, 255, dtype=torch.uint8)), None)
+
+
+def test_a_gradient_that_would_be_missing_is_an_error():
+    from weight_only_quantized_prologue_b200 import rows
+
+    x, y, w = torch.ones(3, requires_grad=True), torch.zeros(3), torch.ones(3)
+    out = rows.no_backward("rmsnorm", y, x, None, w)
+    assert out.requires_grad and out.data_ptr() == y.data_ptr() and not y.requires_grad
+    with pytest.raises(RuntimeError, match="rmsnorm is inference only"):
+        (out + x).sum().backward()
+    assert rows.no_backward("rmsnorm", y, w, None) is y
+    with torch.no_grad():
+        assert rows.no_backward("rmsnorm", y, x) is y

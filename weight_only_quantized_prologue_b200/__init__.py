@@ -375,13 +375,18 @@ class QuantizedExperts:
         """y[m] = x[m] . deq(W_e)^T + b_e for offsets[e] <= m < offsets[e + 1];
         x bf16 [M, K], offsets int32 [E + 1] on the device, not decreasing; y
         (``out``, allocated if None) bf16 [M, N].  Rows that no expert has are
-        left as they were (undefined in an allocated y)."""
+        left as they were (undefined in an allocated y).  Inference only, as the
+        row operators: a gradient that reaches y's raises."""
         torch = _torch()
         M = self._check_x(x, torch.bfloat16)
         self._check_offsets(offsets)
         out = self._out(out, M, torch.bfloat16)
         if M:
             _block_call(self, x, M, offsets.data_ptr(), out, stream)
+        if x.requires_grad:
+            from . import rows
+
+            return rows.no_backward("QuantizedExperts", out, x)
         return out
 
     def from_codes(self, q, scales, offsets, out=None, stream=None):

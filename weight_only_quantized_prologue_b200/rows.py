@@ -14,7 +14,9 @@ output:
 
 Results are allocated if not given (``out``, ``scales``, ``residual_out``) and
 must not overlap the inputs, except where a function says so.  Inference only:
-no gradient is recorded.  A call runs on
+there is no backward.  In grad mode, with an input that requires a gradient, the
+floating results carry a step that raises when a gradient reaches it, as the
+``dqgemm::linear`` op does.  A call runs on
 ``stream``, or on the current stream of the tensors' device, which must be the
 current device.
 """
@@ -40,6 +42,27 @@ def check_current(dev):
     if not _one_device and torch.cuda.current_device() != dev:
         raise ValueError(f"the tensors live on cuda:{dev}; make it the current device "
                          "(torch.cuda.set_device / torch.cuda.device) before the call")
+
+
+class _NoBackward(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, name, y, *inputs):
+        ctx.name = name
+        return y
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} is inference only: it has no backward")
+
+
+def no_backward(name, y, *inputs):
+    """y, with a step that raises in backward where an input wants a gradient
+    (without it the gradient would be missing without a word)."""
+    if torch.is_grad_enabled():
+        wanted = [t for t in inputs if t is not None and t.requires_grad]
+        if wanted:
+            return _NoBackward.apply(name, y, *wanted)
+    return y
 
 
 def _rows(x, name, halves=1):
@@ -162,6 +185,11 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out
                                           _native.device_stream(stream, dev))
         if st:
             raise _native.DQError(st, "dqgemm_rmsnorm")
+    if torch.is_grad_enabled():
+        if quant is None:
+            out = no_backward("rmsnorm", out, x, weight, residual)
+        if residual is not None:
+            residual_out = no_backward("rmsnorm", residual_out, x, residual)
     if residual is None:
         return out if scales is None else (out, scales)
     return (out, residual_out) if scales is None else (out, scales, residual_out)
@@ -182,6 +210,8 @@ def silu_mul(x, quant=None, s_out=None, out_dtype=None, out=None, scales=None, s
                                            _native.device_stream(stream, dev))
         if st:
             raise _native.DQError(st, "dqgemm_silu_mul")
+    if quant is None:
+        out = no_backward("silu_mul", out, x)
     return out if scales is None else (out, scales)
 
 
