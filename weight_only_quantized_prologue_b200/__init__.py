@@ -87,6 +87,23 @@ def _torch():
     return _torch_mod
 
 
+def _empty(shape, dtype, device, stream):
+    """A new dense tensor for a call on `stream`, in that stream's memory: what
+    the allocator hands out for the current stream may still be in use by work
+    queued there, and goes back to that stream's next tensor when a temporary
+    is dropped, while the call may still run."""
+    torch = _torch()
+    # (empty_strided: the cheapest of torch's allocating calls on the host)
+    strides = (shape[1], 1) if len(shape) == 2 else (1,)
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        s = _native._stream(stream)
+        stream = torch.cuda.ExternalStream(s, device=device) if s else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
 def _storage_bytes(fmt, K, N):
     ps, pd, ss, sd = storage_shapes(fmt, K, N)
     return (int(_np.prod(ps)) * _np.dtype(pd).itemsize, int(_np.prod(ss)) * _np.dtype(sd).itemsize)
@@ -106,7 +123,7 @@ def static_mlp(l1, l2, x, out=None, h_out=None, stream=None):
     if l2._dev != l1._dev:
         raise ValueError("both layers must live on the same device")
     M = l1._check_x(x, torch.bfloat16)
-    out = l2._out(out, M, torch.bfloat16)
+    out = l2._out(out, M, torch.bfloat16, stream)
     if h_out is not None:
         _require(h_out, "h_out", shape=(M, l1.N), dtype=torch.bfloat16, device=l1.device)
     if M == 0:
@@ -124,13 +141,8 @@ def _block_call(layer, x, M, offsets, out, stream):
     s = _native.device_stream(stream, dev)
     size = ws = 0
     if M > layer._few_rows:
-        torch = _torch()
         size = M * (layer.K + 4 * ((layer.K + 127) // 128)) + 256
-        if stream is None:
-            tmp = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=layer.device)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=layer.device)):
-                tmp = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=layer.device)
+        tmp = _empty((size,), _torch().uint8, layer.device, stream)
         ws = tmp.data_ptr()
     _native._check(_native.lib().dqgemm_run_fp8_block(layer._h, x.data_ptr(), M, offsets, out.data_ptr(), ws or None, size, s),
                    "dqgemm_run_fp8_block")
@@ -209,10 +221,9 @@ class QuantizedLinear:
                                  f"(torch.cuda.set_device / torch.cuda.device) before calling it")
         return x.shape[0]
 
-    def _out(self, out, M, dtype):
+    def _out(self, out, M, dtype, stream):
         if out is None:
-            # (empty_strided: the cheapest of torch's allocating calls on the host)
-            return _torch().empty_strided((M, self.N), (self.N, 1), dtype=dtype, device=self.device)
+            return _empty((M, self.N), dtype, self.device, stream)
         if not _fits(out, self.N, dtype, M, self._dev):
             _require(out, "out", shape=(M, self.N), dtype=dtype, device=self.device)
         return out
@@ -222,13 +233,13 @@ class QuantizedLinear:
         allocated if None) bf16 [M, N]."""
         torch = _torch()
         M = self._check_x(x, torch.bfloat16)
-        out = self._out(out, M, torch.bfloat16)
+        out = self._out(out, M, torch.bfloat16, stream)
         if M == 0:
             return out
         if self.fmt == "fp8_block":
             _block_call(self, x, M, None, out, stream)
         elif self.fmt == "fp8_static" and M >= self._static_prequant_m:
-            q = torch.empty((M, self.K), dtype=torch.uint8, device=self.device)
+            q = _empty((M, self.K), torch.uint8, self.device, stream)
             dqgemm_quantize_act_fp8(x, M, self.K, self.act_scale, q, stream)
             dqgemm_run_fp8_static_quantized(self._h, q, M, out, stream)
         else:
@@ -241,11 +252,11 @@ class QuantizedLinear:
         e4m3 codes, e4m3(f32(y) / s_out) (uint8 [M, N]); x as for __call__."""
         torch = _torch()
         M = self._check_x(x, torch.bfloat16)
-        out = self._out(out, M, torch.uint8)
+        out = self._out(out, M, torch.uint8, stream)
         if M == 0:
             return out
         if self.fmt == "fp8_static" and M >= self._static_prequant_m:
-            q = torch.empty((M, self.K), dtype=torch.uint8, device=self.device)
+            q = _empty((M, self.K), torch.uint8, self.device, stream)
             dqgemm_quantize_act_fp8(x, M, self.K, self.act_scale, q, stream)
             dqgemm_run_fp8_static_quantized_out(self._h, q, M, out, s_out, stream)
         else:
@@ -265,7 +276,7 @@ class QuantizedLinear:
         M = self._check_x(q, torch.uint8, "q")
         if scales is not None and not _fits(scales, (self.K + 127) // 128, torch.float32, M, self._dev):
             _require(scales, "scales", shape=(M, (self.K + 127) // 128), dtype=torch.float32, device=self.device)
-        out = self._out(out, M, torch.bfloat16)
+        out = self._out(out, M, torch.bfloat16, stream)
         if M == 0:
             return out
         if scales is not None:
@@ -277,9 +288,7 @@ class QuantizedLinear:
         return out
 
     def dequantize(self, stream=None):
-        import torch
-
-        w = torch.empty((self.N, self.K), dtype=torch.bfloat16, device=self.device)
+        w = _empty((self.N, self.K), _torch().bfloat16, self.device, stream)
         dqgemm_dequantize(self._h, w, stream)
         return w
 
@@ -380,7 +389,7 @@ class QuantizedExperts:
         torch = _torch()
         M = self._check_x(x, torch.bfloat16)
         self._check_offsets(offsets)
-        out = self._out(out, M, torch.bfloat16)
+        out = self._out(out, M, torch.bfloat16, stream)
         if M:
             _block_call(self, x, M, offsets.data_ptr(), out, stream)
         if x.requires_grad:
@@ -396,7 +405,7 @@ class QuantizedExperts:
         if not _fits(scales, (self.K + 127) // 128, torch.float32, M, self._dev):
             _require(scales, "scales", shape=(M, (self.K + 127) // 128), dtype=torch.float32, device=self.device)
         self._check_offsets(offsets)
-        out = self._out(out, M, torch.bfloat16)
+        out = self._out(out, M, torch.bfloat16, stream)
         if M:
             _native._check(_native.lib().dqgemm_run_experts_quantized(
                 self._h, q.data_ptr(), scales.data_ptr(), M, offsets.data_ptr(), out.data_ptr(),
@@ -404,9 +413,9 @@ class QuantizedExperts:
         return out
 
     def dequantize(self, stream=None):
-        w = _torch().empty((self.E, self.N, self.K), dtype=_torch().bfloat16, device=self.device)
+        w = _empty((self.E * self.N, self.K), _torch().bfloat16, self.device, stream)
         dqgemm_dequantize(self._h, w, stream)
-        return w
+        return w.view(self.E, self.N, self.K)
 
     plan = QuantizedLinear.plan
     last_error = QuantizedLinear.last_error

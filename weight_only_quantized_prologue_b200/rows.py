@@ -18,18 +18,17 @@ there is no backward.  In grad mode, with an input that requires a gradient, the
 floating results carry a step that raises when a gradient reaches it, as the
 ``dqgemm::linear`` op does.  A call runs on
 ``stream``, or on the current stream of the tensors' device, which must be the
-current device.
+current device; its new tensors belong to that stream.
 """
 
 import math
 
 import torch
 
-from . import _native, _require
+from . import _empty, _native, _require
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # _native.ROW_TYPES, ROW_OUTS
 _U8, _F32 = torch.uint8, torch.float32
-_empty = torch.empty_strided   # (the cheapest of torch's allocating calls on the host)
 _one_device = None
 
 
@@ -90,10 +89,6 @@ def _rows(x, name, halves=1):
     return M, width // halves, ld if M > 1 else width
 
 
-def _new(x, M, K, dtype):
-    return _empty((M, K), (K, 1), dtype=dtype, device=x.device)
-
-
 def _given(t, name, M, K, dtype, x):
     """A given [M, K] operand of x's device: checked the short way, and only a
     misfit by _require, which names it."""
@@ -102,7 +97,7 @@ def _given(t, name, M, K, dtype, x):
         _require(t, name, shape=(M, K), dtype=dtype, device=x.device)
 
 
-def _outputs(x, M, K, quant, s_out, out_dtype, out, scales):
+def _outputs(x, M, K, quant, s_out, out_dtype, out, scales, stream=None):
     """(kind, s_out, out, scales) with what is not given allocated."""
     if quant == "fp8_block":
         if out_dtype is not None:
@@ -111,12 +106,12 @@ def _outputs(x, M, K, quant, s_out, out_dtype, out, scales):
             raise ValueError("s_out goes with quant='fp8_static'")
         dev = x.device
         if out is None:
-            out = _empty((M, K), (K, 1), dtype=_U8, device=dev)
+            out = _empty((M, K), _U8, dev, stream)
         else:
             _given(out, "out", M, K, _U8, x)
         kb = (K + 127) // 128
         if scales is None:
-            scales = _empty((M, kb), (kb, 1), dtype=_F32, device=dev)
+            scales = _empty((M, kb), _F32, dev, stream)
         else:
             _given(scales, "scales", M, kb, _F32, x)
         return 3, 1.0, out, scales
@@ -138,7 +133,7 @@ def _outputs(x, M, K, quant, s_out, out_dtype, out, scales):
     else:
         raise ValueError(f"unknown quant {quant!r}; None, 'fp8_block' or 'fp8_static'")
     if out is None:
-        out = _new(x, M, K, dt)
+        out = _empty((M, K), dt, x.device, stream)
     else:
         _given(out, "out", M, K, dt, x)
     return kind, s_out, out, None
@@ -170,7 +165,7 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out
     if residual is not None:
         _given(residual, "residual", M, K, dt, x)
         if residual_out is None:
-            residual_out = _new(x, M, K, dt)
+            residual_out = _empty((M, K), dt, x.device, stream)
         elif residual_out is not residual:
             _given(residual_out, "residual_out", M, K, dt, x)
         rp, np = residual.data_ptr(), residual_out.data_ptr()
@@ -178,7 +173,7 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out
         raise ValueError("residual_out needs a residual")
     if not 0 <= eps < math.inf:
         raise ValueError(f"eps must be finite and not negative, got {eps}")
-    kind, s_out, out, scales = _outputs(x, M, K, quant, s_out, out_dtype, out, scales)
+    kind, s_out, out, scales = _outputs(x, M, K, quant, s_out, out_dtype, out, scales, stream)
     if M:
         st = _native.lib().dqgemm_rmsnorm(_TYPES[dt], x.data_ptr(), ld, rp, np, wt or 0, wp, eps, M, K, kind, s_out,
                                           out.data_ptr(), None if scales is None else scales.data_ptr(),
@@ -203,7 +198,7 @@ def silu_mul(x, quant=None, s_out=None, out_dtype=None, out=None, scales=None, s
     dev = x.get_device()
     if _one_device is not True:
         check_current(dev)
-    kind, s_out, out, scales = _outputs(x, M, K, quant, s_out, out_dtype, out, scales)
+    kind, s_out, out, scales = _outputs(x, M, K, quant, s_out, out_dtype, out, scales, stream)
     if M:
         st = _native.lib().dqgemm_silu_mul(_TYPES[x.dtype], x.data_ptr(), ld, M, K, kind, s_out, out.data_ptr(),
                                            None if scales is None else scales.data_ptr(),
@@ -222,7 +217,7 @@ def quantize_act_fp8_block(x, out=None, scales=None, stream=None):
     dev = x.get_device()
     if _one_device is not True:
         check_current(dev)
-    _, _, out, scales = _outputs(x, M, K, "fp8_block", None, None, out, scales)
+    _, _, out, scales = _outputs(x, M, K, "fp8_block", None, None, out, scales, stream)
     if M:
         _native._check(_native.lib().dqgemm_quantize_act_fp8_block(
             _TYPES[x.dtype], x.data_ptr(), ld, M, K, out.data_ptr(), scales.data_ptr(),
