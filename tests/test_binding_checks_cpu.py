@@ -141,3 +141,32 @@ def test_buffers_may_be_given_as_integer_addresses():
     assert _native._ptr(a) == a.ctypes.data
     t = torch.zeros(4)
     assert _native._ptr(t) == t.data_ptr()
+
+
+class OnDevice1:
+    """Stands in for a tensor of a second GPU: the checks only read metadata."""
+
+    def __init__(self, *shape, dtype=torch.uint8):
+        self.t, self.is_cuda, self.device = torch.zeros(*shape, dtype=dtype), True, torch.device("cuda", 1)
+
+    def __getattr__(self, n):
+        return getattr(self.t, n)
+
+
+def test_a_weight_of_another_device_than_the_current_one_is_refused(monkeypatch):
+    # the handle would belong to the current device and read the other's memory by its bare pointer
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    f32 = torch.float32
+    with pytest.raises(ValueError, match="packed is on cuda:1"):
+        dq.QuantizedLinear("fp8_block", 128, 128, OnDevice1(128, 128), OnDevice1(1, 1, dtype=f32))
+    with pytest.raises(ValueError, match="packed is on cuda:1"):
+        dq.QuantizedExperts("fp8_block", 2, 128, 128, OnDevice1(2, 128, 128), OnDevice1(2, 1, 1, dtype=f32))
+    with pytest.raises(ValueError, match="W is on cuda:1"):
+        dq.QuantizedLinear.from_float("int4", OnDevice1(128, 128, dtype=f32))
+    with pytest.raises(ValueError, match="W is on cuda:1"):
+        dq.QuantizedExperts.from_float("fp8_block", OnDevice1(2, 128, 128, dtype=f32))
+    lin = _layer("fp8_block")
+    lin.device, lin._dev = torch.device("cuda", 1), 1
+    with pytest.raises(ValueError, match="the layer is on cuda:1"):
+        lin.dequantize()

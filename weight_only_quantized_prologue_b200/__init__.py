@@ -87,6 +87,15 @@ def _torch():
     return _torch_mod
 
 
+def _on_current_device(device, what):
+    """The library launches on, and a handle belongs to, the current device: a
+    weight or layer on another one would be read there through bare pointers."""
+    cuda = _torch().cuda
+    if cuda.device_count() > 1 and cuda.current_device() != device.index:
+        raise ValueError(f"{what} on {device}; make it the current device (torch.cuda.set_device / "
+                         f"torch.cuda.device) before the call")
+
+
 def _empty(shape, dtype, device, stream):
     """A new dense tensor for a call on `stream`, in that stream's memory: what
     the allocator hands out for the current stream may still be in use by work
@@ -180,6 +189,7 @@ class QuantizedLinear:
         if bias is not None:
             _require(bias, "bias", shape=(N,), dtype=torch.bfloat16, device=packed.device)
         self.fmt, self.K, self.N = fmt, K, N
+        _on_current_device(packed.device, "packed is")
         sms = torch.cuda.get_device_properties(packed.device).multi_processor_count
         n_tiles = (N + 127) // 128
         self._static_prequant_m = (self.STATIC_PREQUANT_M_WIDE if 2 * n_tiles > sms and n_tiles <= sms
@@ -199,6 +209,7 @@ class QuantizedLinear:
 
         if not getattr(W, "is_cuda", False) or W.dim() != 2:
             raise ValueError("W must be a 2-D CUDA tensor [N, K]")
+        _on_current_device(W.device, "W is")
         W = W.detach().to(torch.float32).contiguous()
         N, K = W.shape
         ps, pd, ss, sd = storage_shapes(fmt, K, N)
@@ -288,6 +299,7 @@ class QuantizedLinear:
         return out
 
     def dequantize(self, stream=None):
+        _on_current_device(self.device, "the layer is")
         w = _empty((self.N, self.K), _torch().bfloat16, self.device, stream)
         dqgemm_dequantize(self._h, w, stream)
         return w
@@ -345,6 +357,7 @@ class QuantizedExperts:
                  device=packed.device)
         if bias is not None:
             _require(bias, "bias", shape=(E, N), dtype=torch.bfloat16, device=packed.device)
+        _on_current_device(packed.device, "packed is")
         self.fmt, self.E, self.K, self.N = fmt, E, K, N
         self.device = packed.device
         self._dev = self.device.index
@@ -360,6 +373,7 @@ class QuantizedExperts:
 
         if not getattr(W, "is_cuda", False) or W.dim() != 3:
             raise ValueError("W must be a 3-D CUDA tensor [E, N, K]")
+        _on_current_device(W.device, "W is")
         if fmt != "fp8_block":
             raise ValueError(f"experts take the format 'fp8_block', not {fmt!r}")
         E, N, K = W.shape
@@ -413,6 +427,7 @@ class QuantizedExperts:
         return out
 
     def dequantize(self, stream=None):
+        _on_current_device(self.device, "the layer is")
         w = _empty((self.E * self.N, self.K), _torch().bfloat16, self.device, stream)
         dqgemm_dequantize(self._h, w, stream)
         return w.view(self.E, self.N, self.K)
