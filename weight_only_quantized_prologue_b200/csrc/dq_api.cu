@@ -350,11 +350,13 @@ int bn_index(int bn) { return bn == 16 ? 0 : bn == 32 ? 1 : bn == 64 ? 2 : 3; }
 
 // How many clusters of `split` CTAs can be resident at once (cached per handle).
 int cluster_capacity(dqgemm_s* h, int bn, int split) {
-  int& c = h->max_clusters[bn_index(bn)][split];
+  std::atomic<int>& known = h->max_clusters[bn_index(bn)][split];
+  int c = known.load(std::memory_order_relaxed);
   if (c == 0) {
     int n = 0;
     DQ_FMT_SWITCH(h->fmt, n = max_clusters_fmt<F>(bn, split));
     c = n > 0 ? n : -1;
+    known.store(c, std::memory_order_relaxed);
   }
   return c;
 }

@@ -103,11 +103,13 @@ int skinny_clusters(int split) {
 // how many clusters of `split` CTAs run at once (they have to lie in one GPC
 // each, so not as many as the SMs would hold); asked once per handle
 int cluster_capacity(dqgemm_s* h, int bn, int split) {
-  int& c = h->max_clusters[bn == 16 ? 0 : bn == 32 ? 1 : bn == 64 ? 2 : 3][split];
+  std::atomic<int>& known = h->max_clusters[bn == 16 ? 0 : bn == 32 ? 1 : bn == 64 ? 2 : 3][split];
+  int c = known.load(std::memory_order_relaxed);
   if (c == 0) {
     const int n = bn == 16 ? skinny_clusters<16>(split) : bn == 32 ? skinny_clusters<32>(split)
                 : bn == 64 ? skinny_clusters<64>(split) : skinny_clusters<128>(split);
     c = n > 0 ? n : -1;
+    known.store(c, std::memory_order_relaxed);
   }
   return c;
 }

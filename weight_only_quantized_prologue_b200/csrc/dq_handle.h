@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cstdlib>
 #include <mutex>
 
@@ -25,7 +26,9 @@ struct dqgemm_s {
   float sigma = 1.f, s_x = 1.f;
   int mx_bias = 126;
   long long weight_bytes = 0;       // canonical packed + scale bytes
-  int max_clusters[4][9] = {};      // co-resident clusters per (BN index, cluster size), 0 = unknown
+  // co-resident clusters per (BN index, cluster size), 0 = unknown (calls from
+  // several threads may ask at once: each finds the same)
+  std::atomic<int> max_clusters[4][9] = {};
   // FP4 x FP4: the activation workspace (codes, scale words, the NVFP4 amax
   // partials, ticket and g_x), grown on demand and reused by every call
   uint8_t* ws = nullptr;

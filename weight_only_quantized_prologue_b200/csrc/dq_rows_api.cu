@@ -1,6 +1,7 @@
 // dq_rows_api.cu -- the row operators of include/dqgemm.h: dqgemm_rmsnorm,
 // dqgemm_silu_mul, dqgemm_quantize_act_fp8_block.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "dq_handle.h"
@@ -39,25 +40,27 @@ dqgemm_status check_rows(const RowArgs& a, int type, int out, int halves, int* a
 
 // multiprocessors of the current device
 int sm_count() {
-  static int counts[64] = {};
+  static std::atomic<int> counts[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (counts[dev] == 0) {   // (every thread would write the same value)
-    int n = 0;
-    counts[dev] = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0 ? n : 148;
+  int n = counts[dev].load(std::memory_order_relaxed);
+  if (n == 0) {   // (every thread finds the same)
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    counts[dev].store(n, std::memory_order_relaxed);
   }
-  return counts[dev];
+  return n;
 }
 
 // CTAs of a kernel that are resident at once, on all multiprocessors: what a
 // launch over many rows starts, since each goes on to the next rows itself
 template <typename K>
-long long resident_ctas(K kern, int threads, int (&cache)[33]) {
-  int& n = cache[threads / 32];   // (every thread would write the same value)
+long long resident_ctas(K kern, int threads, std::atomic<int> (&cache)[33]) {
+  std::atomic<int>& known = cache[threads / 32];   // (every thread finds the same)
+  int n = known.load(std::memory_order_relaxed);
   if (n == 0) {
-    int v = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, 0) != cudaSuccess) cudaGetLastError();
-    n = std::max(1, v);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess) cudaGetLastError();
+    n = std::max(1, n);
+    known.store(n, std::memory_order_relaxed);
   }
   return (long long)n * sm_count();
 }
@@ -78,7 +81,7 @@ dqgemm_status launch_rows(void (*kern)(KArgs...), dim3 grid, dim3 block, void* s
 
 template <typename T, int NV, int OUT, int AL, int MT>
 dqgemm_status norm_grid(const RowArgs& a, long long need, dim3 block, void* stream) {
-  static int cache[33] = {};
+  static std::atomic<int> cache[33] = {};
   const long long most = resident_ctas(rmsnorm_kernel<T, NV, OUT, AL, MT>, (int)(block.x * block.y), cache);
   return launch_rows(rmsnorm_kernel<T, NV, OUT, AL, MT>, dim3((unsigned)std::min(need, most)), block, stream, a);
 }
@@ -112,7 +115,7 @@ dqgemm_status plain_launch(const RowArgs& a, void* stream) {
   const long long items = (long long)parts * a.M;
   // (few warps: one a CTA, so that they spread over the multiprocessors)
   const int per = (int)std::max<long long>(1, std::min<long long>(8, items / sm_count()));
-  static int cache[33] = {};
+  static std::atomic<int> cache[33] = {};
   const int ctas = (int)std::min((items + per - 1) / per, resident_ctas(rows_kernel<T, GATE, OUT, AL>, 32 * per, cache));
   return launch_rows(rows_kernel<T, GATE, OUT, AL>, dim3(ctas), dim3(32 * per), stream, a, parts);
 }
