@@ -384,3 +384,29 @@ def test_gradients_raise_where_they_would_be_missing():
     assert torch.equal(y, ex(x, off))
     with pytest.raises(RuntimeError, match="inference only"):
         y.float().sum().backward()
+
+
+@pytest.mark.parametrize("exponent", [-80, 0, 100])
+def test_every_significand_of_a_blocks_maximum(exponent):
+    """Scales and codes of blocks with each of the 2^23 significands of amax (of a
+    binade), the other elements next to the borders between codes times the scale:
+    the fp32 quotients decide those codes, so they test the scale, its reciprocal
+    and the quotient's correction.  The definition in 64 bits: a quotient of two
+    fp32 numbers rounded to fp64 and then to fp32 is the one rounded once (53 >=
+    2 * 24 + 2)."""
+    t = torch.arange(127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).double()
+    border = (t[:-1] + t[1:]) / 2                                   # 126 of them, exact
+    step = 1 << 17
+    for at in range(0, 1 << 23, step):
+        m = torch.arange(at, at + step, device="cuda", dtype=torch.int32)
+        a = (m + ((127 + exponent) << 23)).view(torch.float32)
+        s = (a.double() / torch.tensor(448.0, dtype=torch.float64, device="cuda")).float()
+        v = (s.double()[:, None] * border).float()                  # the nearest to the border, and one unit off
+        off = (torch.arange(126, device="cuda") + m[:, None]) % 3 - 1
+        v = (v.view(torch.int32) + off.int()).view(torch.float32)
+        v[:, -1] = torch.minimum(v[:, -1], a)                       # (the largest border is below amax)
+        x = torch.cat([a[:, None], v, -v[:, :1]], 1)
+        q, sc = dq.quantize_act_fp8_block(x)
+        assert torch.equal(sc[:, 0], s)
+        want = (x.double() / s.double()[:, None]).float().to(torch.float8_e4m3fn)
+        assert torch.equal(q, want.view(torch.uint8)), at

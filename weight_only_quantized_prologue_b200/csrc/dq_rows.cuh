@@ -369,9 +369,14 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 
 // The scale of a block, s = f32(amax / 448), and r = f32(1 / s) (1 for s = 0),
 // from the bits of amax.  Straight-line: both quotients by Markstein's
-// correction steps (see e4m3_quotient), r from the hardware's reciprocal
-// (within 2^-23) by one step, which gives the correctly rounded value unless
-// s has the largest significand.  `fast` says that s and r are what they
+// correction steps (see e4m3_quotient).  s: amax * f32(1/448) is within one
+// unit in the last place of the quotient, 448 = 7 * 2^6 leaves the residual
+// exact.  r: from the hardware's reciprocal, whose documented error is one unit
+// in the last place, by one step; the step gives the correctly rounded value
+// from any estimate within one unit, unless s has the largest significand.  (An
+// error of 2^-23 relative would not do: where the significand of s is below 4/3
+// that is up to 1.5 units, from which the step can miss.)  All 2^23
+// significands of amax are tested.  `fast` says that s and r are what they
 // should be and that r is a normal number: amax is 0, or from 2^-87 to the
 // largest finite value, and s has another significand.  The division's own
 // code has branches for special operands (zero among them, the commonest
