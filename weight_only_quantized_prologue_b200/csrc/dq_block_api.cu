@@ -68,11 +68,17 @@ int force_split() {
 }
 
 // Whether a call on bf16 activations quantizes them in the product itself, one
-// launch instead of two.  A layer: up to 8 rows, which the quantizing warps
-// handle within the weight's stream (1 x 4096 x 14336 15.3 us, on codes 14.2;
-// 16 rows 20.5 against 15.7 with the quantizer ahead).  Experts, whose CTAs go
-// through several tiles: 16 rows and at most 16 blocks a CTA (7 x 1024 x 768:
-// 6.2 us, on codes 5.0; but 64 x 4096 x 2048, 24 of 32 experts: 46 against 36).
+// launch instead of two.  A layer: up to 8 rows, which the quantizing warps hold
+// in registers at once.  It saves a launch and the caller's temporary, not time
+// on the GPU.  Weights from HBM, us, one launch / quantizer and product:
+//                               1 row       8 rows      9 rows      16 rows
+//   4096 x 14336, GPU only   14.4 / 13.3  14.7 / 13.7  18.8 / 13.8  19.5 / 13.9
+//   4096 x 4096, GPU only     8.3 /  8.3   8.5 /  8.5   9.6 /  8.5   9.8 /  8.7
+//   4096 x 4096, from Python  8.4 / 11.6   8.5 / 11.7   9.6 / 11.7   9.7 / 11.7
+//   2048 x 2048, from Python  7.4 / 11.6   7.2 / 11.7   7.4 / 11.6   7.6 / 11.5
+// Experts, whose CTAs go through several tiles: 16 rows and at most 16 blocks a
+// CTA (7 x 1024 x 768: 6.2 us, on codes 5.0; but 64 x 4096 x 2048, 24 of 32
+// experts: 46 against 36).
 bool quantizes(const dqgemm_s* h, int M) {
   if (!h->experts) return M <= 8;
   return M <= 16 && h->k_stages * ceil_div((long long)std::min(h->E, M) * h->n_tiles, h->num_sms) <= 16;
@@ -128,14 +134,25 @@ int pick_split(dqgemm_s* h, long long T, int bn) {
   return s;
 }
 
+// Above 64 rows: 128 x 128 tiles by single CTAs or 256 x 256 by pairs, whichever
+// takes less by this fit, in ns, of both kernels' times: rounds of tiles, each so
+// much per block of K and so much per tile (its output), a split's meeting.
+// Measured with weights from HBM at K = 512, 1152 and 4096, N = 1024, 2048,
+// 4096, 5000, 8192 and 14336 and 17 counts of rows from 65 to 2048: the choice is
+// the faster kernel or within 7 %, 0.2 % on average.  Some of it (us, single / pair):
+//   rows                  65          256          512          777         1024         2048
+//   512 x 2048     6.4 / 6.3    7.4 / 6.3    7.9 / 6.3    6.7 / 6.4    6.9 / 6.4   10.8 / 7.0
+//   1152 x 5000    8.9 / 8.7    8.8 / 8.7   14.5 / 9.3  15.0 / 14.6  20.4 / 14.7  32.4 / 20.7
+//   4096 x 4096  10.9 / 18.8  14.7 / 19.0  20.4 / 19.4  37.2 / 20.1  37.2 / 20.3  71.4 / 35.9
+//   4096 x 14336 20.4 / 21.7  38.6 / 22.1  71.8 / 37.6  106.0 / 68.1  122.6 / 68.6  224.0 / 120.3
 BlockPlan dense_plan(dqgemm_s* h, int M) {
   BlockPlan pl{};
   pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   if (M > 64) {
     const long long t1 = ceil_div(M, 128) * h->n_tiles, t2 = ceil_div(M, 256) * ceil_div(h->N, 256);
     const int s = pick_split(h, t1, 128);
-    const long long c1 = ceil_div(t1 * s, h->num_sms) * ceil_div(h->k_stages, s) * 520;
-    const long long c2 = ceil_div(t2, h->num_sms / 2) * h->k_stages * 600;
+    const long long c1 = ceil_div(t1 * s, h->num_sms) * (470 * ceil_div(h->k_stages, s) + 1850) + (s > 1 ? 2000 : 250);
+    const long long c2 = ceil_div(t2, h->num_sms / 2) * (460 * h->k_stages + 1900);
     if (c2 <= c1) {
       pl.pair = true;
       pl.bn = 256;
@@ -155,16 +172,21 @@ BlockPlan dense_plan(dqgemm_s* h, int M) {
 }
 
 // The rows of each expert are known on the device only; the tile is picked by
-// their mean.  Measured with 32 experts of 4096 x 2048 (us):
-//   rows an expert      16     24     32     64     96    128    192
-//   32-row tiles        45     50     53
-//   64-row tiles               51     51     69     80    100
-//   256-row (pair)                           79     81     83    102
+// their mean over all experts.  Measured with 32 experts of 4096 x 2048 and rows
+// that fall on them at random (us; 64 experts of 2048 x 1536 cross at the same places):
+//   rows an expert   4     8    16    24    32    48    64    80    96   128   192
+//   16-row tiles    45.2  46.3  47.7  63.9  83
+//   32-row tiles    45.3  46.4  46.9  49.3  51.8  65.5  77.6
+//   64-row tiles    48.3  49.6  50.7  52.7  54.9  58.8  71.9  80.5  88.7   106   137
+//   256-row (pair)  69.6  73.2  76.1  79.5  83.1  79.5  80.0  80.5  82.7  82.3  86.8
+// Rows that gather on few of many experts would want larger tiles than their
+// mean says: 512 rows on one of 32 experts take 19.5 us with the 32-row tiles
+// of a mean of 16 (64-row tiles 14.7), 2048 rows on two of 128 60 us (pairs 22.9).
 BlockPlan grouped_plan(const dqgemm_s* h, int M) {
   BlockPlan pl{};
   const long long mean = ceil_div(M, h->E);
-  pl.pair = mean > 96;
-  pl.bn = pl.pair ? 256 : M <= 16 || mean <= 4 ? 16 : mean <= 24 ? 32 : 64;
+  pl.pair = mean > 80;
+  pl.bn = pl.pair ? 256 : M <= 16 || mean <= 4 ? 16 : mean <= 32 ? 32 : 64;
   pl.n_tiles = (int)ceil_div(h->N, pl.pair ? 256 : 128);
   pl.m_tiles = 0;
   pl.split = 1;
