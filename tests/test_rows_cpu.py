@@ -109,3 +109,22 @@ def test_a_gradient_that_would_be_missing_is_an_error():
     assert rows.no_backward("rmsnorm", y, w, None) is y
     with torch.no_grad():
         assert rows.no_backward("rmsnorm", y, x) is y
+
+
+def test_sizes_beyond_the_librarys_32_bit_numbers_are_refused():
+    from weight_only_quantized_prologue_b200 import rows
+
+    def huge(*shape):        # metadata only: no memory behind it
+        return Fake(torch.empty(shape, dtype=torch.bfloat16, device="meta"))
+
+    for x in (huge(1 << 31, 1), huge((1 << 32) + 5, 1), huge(1, (1 << 28) + 1), huge(2, (1 << 32) + 256)):
+        with pytest.raises(ValueError, match="2.31 rows and at most 2.28"):
+            rows._rows(x, "x")
+    with pytest.raises(ValueError, match="a half"):
+        rows._rows(huge(1, (1 << 29) + 2), "x", 2)
+    assert rows._rows(huge(1, 1 << 29), "x", 2) == (1, 1 << 28, 1 << 29)
+    assert rows._rows(huge((1 << 31) - 1, 1), "x") == ((1 << 31) - 1, 1, 1)
+    lin = dq.QuantizedLinear.__new__(dq.QuantizedLinear)
+    lin._h, lin.fmt, lin.K, lin.N, lin.device, lin._dev, lin._check_current = None, "fp8_block", 16, 16, torch.device("cuda", 0), 0, False
+    with pytest.raises(ValueError, match="2.31 rows"):
+        lin._check_x(Fake(torch.empty(((1 << 32) + 5, 16), dtype=torch.uint8, device="meta")), torch.uint8, "q")

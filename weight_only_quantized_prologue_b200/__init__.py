@@ -230,7 +230,10 @@ class QuantizedLinear:
             if _torch().cuda.current_device() != self._dev:
                 raise ValueError(f"the layer lives on {self.device}; make it the current device "
                                  f"(torch.cuda.set_device / torch.cuda.device) before calling it")
-        return x.shape[0]
+        M = x.shape[0]
+        if M >= 1 << 31:   # (the library takes it as a 32-bit number)
+            raise ValueError(f"{name} must have fewer than 2^31 rows")
+        return M
 
     def _out(self, out, M, dtype, stream):
         if out is None:

@@ -29,6 +29,7 @@ from . import _empty, _native, _require
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # _native.ROW_TYPES, ROW_OUTS
 _U8, _F32 = torch.uint8, torch.float32
+_MAX_M, _MAX_K = 1 << 31, 1 << 28
 _one_device = None
 
 
@@ -69,7 +70,7 @@ def _rows(x, name, halves=1):
     try:                     # the common operand, checked in a few steps
         if x.is_cuda and x.dtype in _TYPES and x.is_contiguous():
             M, width = x.shape
-            if width and not width % halves:
+            if width and not width % halves and M < _MAX_M and width <= _MAX_K:
                 return M, width // halves, width
     except (AttributeError, ValueError):
         pass
@@ -83,6 +84,8 @@ def _rows(x, name, halves=1):
     if width % halves or width == 0:
         raise ValueError(f"{name} must hold {halves} halves of at least one column" if halves > 1
                          else f"{name} must have at least one column")
+    if M >= _MAX_M or width // halves > _MAX_K:   # (the library takes them as 32-bit numbers)
+        raise ValueError(f"{name} must have fewer than 2^31 rows and at most 2^28 columns{' a half' if halves > 1 else ''}")
     ld, inner = x.stride()
     if (inner != 1 and width != 1) or (M > 1 and ld < width):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
