@@ -102,7 +102,6 @@ def _empty(shape, dtype, device, stream):
     queued there, and goes back to that stream's next tensor when a temporary
     is dropped, while the call may still run."""
     torch = _torch()
-    # (empty_strided: the cheapest of torch's allocating calls on the host)
     strides = (shape[1], 1) if len(shape) == 2 else (1,)
     if stream is None:
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
@@ -237,6 +236,8 @@ class QuantizedLinear:
 
     def _out(self, out, M, dtype, stream):
         if out is None:
+            if stream is None:   # (empty_strided: the cheapest of torch's allocating calls on the host)
+                return _torch().empty_strided((M, self.N), (self.N, 1), dtype=dtype, device=self.device)
             return _empty((M, self.N), dtype, self.device, stream)
         if not _fits(out, self.N, dtype, M, self._dev):
             _require(out, "out", shape=(M, self.N), dtype=dtype, device=self.device)

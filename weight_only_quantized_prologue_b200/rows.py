@@ -29,6 +29,7 @@ from . import _empty, _native, _require
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # _native.ROW_TYPES, ROW_OUTS
 _U8, _F32 = torch.uint8, torch.float32
+_new = torch.empty_strided   # (the cheapest of torch's allocating calls on the host)
 _MAX_M, _MAX_K = 1 << 31, 1 << 28
 _one_device = None
 
@@ -58,10 +59,9 @@ class _NoBackward(torch.autograd.Function):
 def no_backward(name, y, *inputs):
     """y, with a step that raises in backward where an input wants a gradient
     (without it the gradient would be missing without a word)."""
-    if torch.is_grad_enabled():
-        wanted = [t for t in inputs if t is not None and t.requires_grad]
-        if wanted:
-            return _NoBackward.apply(name, y, *wanted)
+    wanted = [t for t in inputs if t is not None and t.requires_grad]
+    if wanted and torch.is_grad_enabled():
+        return _NoBackward.apply(name, y, *wanted)
     return y
 
 
@@ -109,12 +109,12 @@ def _outputs(x, M, K, quant, s_out, out_dtype, out, scales, stream=None):
             raise ValueError("s_out goes with quant='fp8_static'")
         dev = x.device
         if out is None:
-            out = _empty((M, K), _U8, dev, stream)
+            out = _new((M, K), (K, 1), dtype=_U8, device=dev) if stream is None else _empty((M, K), _U8, dev, stream)
         else:
             _given(out, "out", M, K, _U8, x)
         kb = (K + 127) // 128
         if scales is None:
-            scales = _empty((M, kb), _F32, dev, stream)
+            scales = _new((M, kb), (kb, 1), dtype=_F32, device=dev) if stream is None else _empty((M, kb), _F32, dev, stream)
         else:
             _given(scales, "scales", M, kb, _F32, x)
         return 3, 1.0, out, scales
@@ -136,7 +136,7 @@ def _outputs(x, M, K, quant, s_out, out_dtype, out, scales, stream=None):
     else:
         raise ValueError(f"unknown quant {quant!r}; None, 'fp8_block' or 'fp8_static'")
     if out is None:
-        out = _empty((M, K), dt, x.device, stream)
+        out = _new((M, K), (K, 1), dtype=dt, device=x.device) if stream is None else _empty((M, K), dt, x.device, stream)
     else:
         _given(out, "out", M, K, dt, x)
     return kind, s_out, out, None
@@ -168,7 +168,8 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out
     if residual is not None:
         _given(residual, "residual", M, K, dt, x)
         if residual_out is None:
-            residual_out = _empty((M, K), dt, x.device, stream)
+            residual_out = (_new((M, K), (K, 1), dtype=dt, device=x.device) if stream is None
+                            else _empty((M, K), dt, x.device, stream))
         elif residual_out is not residual:
             _given(residual_out, "residual_out", M, K, dt, x)
         rp, np = residual.data_ptr(), residual_out.data_ptr()
@@ -183,7 +184,7 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, quant=None, s_out=None, out
                                           _native.device_stream(stream, dev))
         if st:
             raise _native.DQError(st, "dqgemm_rmsnorm")
-    if torch.is_grad_enabled():
+    if x.requires_grad or weight is not None and weight.requires_grad or residual is not None and residual.requires_grad:
         if quant is None:
             out = no_backward("rmsnorm", out, x, weight, residual)
         if residual is not None:
@@ -208,7 +209,7 @@ def silu_mul(x, quant=None, s_out=None, out_dtype=None, out=None, scales=None, s
                                            _native.device_stream(stream, dev))
         if st:
             raise _native.DQError(st, "dqgemm_silu_mul")
-    if quant is None:
+    if quant is None and x.requires_grad:
         out = no_backward("silu_mul", out, x)
     return out if scales is None else (out, scales)
 
