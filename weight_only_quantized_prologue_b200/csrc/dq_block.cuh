@@ -1072,7 +1072,18 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
         const int nn = min(128, p.N - n0);
         uint8_t* mine = smem + C::OUT_OFF + (threadIdx.x - 128) * C::OUT_PITCH;
         bulk_wait_read();   // this thread's last row has left
-        if (bias) {
+        if (bias && nn == 128 && (reinterpret_cast<uintptr_t>(bias) & 15) == 0) {   // (one by one: 1.9 us a tile)
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            const uint4 u = *reinterpret_cast<const uint4*>(bias + c);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              acc[c + 2 * k] += __uint_as_float(w[k] << 16);
+              acc[c + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+            }
+          }
+        } else if (bias) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) acc[c] += c < nn ? __bfloat162float(bias[c]) : 0.f;
         }

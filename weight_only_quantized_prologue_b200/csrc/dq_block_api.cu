@@ -139,7 +139,8 @@ int pick_split(dqgemm_s* h, long long T, int bn) {
 // much per block of K and so much per tile (its output), a split's meeting.
 // Measured with weights from HBM at K = 512, 1152 and 4096, N = 1024, 2048,
 // 4096, 5000, 8192 and 14336 and 17 counts of rows from 65 to 2048: the choice is
-// the faster kernel or within 7 %, 0.2 % on average.  Some of it (us, single / pair):
+// the faster kernel or within 7 %, 0.2 % on average.  A bias costs a pair's tile
+// half a us more (1040 x 5000, 777 rows: 15.7 / 16.2).  Some of it (us, single / pair):
 //   rows                  65          256          512          777         1024         2048
 //   512 x 2048     6.4 / 6.3    7.4 / 6.3    7.9 / 6.3    6.7 / 6.4    6.9 / 6.4   10.8 / 7.0
 //   1152 x 5000    8.9 / 8.7    8.8 / 8.7   14.5 / 9.3  15.0 / 14.6  20.4 / 14.7  32.4 / 20.7
@@ -152,7 +153,7 @@ BlockPlan dense_plan(dqgemm_s* h, int M) {
     const long long t1 = ceil_div(M, 128) * h->n_tiles, t2 = ceil_div(M, 256) * ceil_div(h->N, 256);
     const int s = pick_split(h, t1, 128);
     const long long c1 = ceil_div(t1 * s, h->num_sms) * (470 * ceil_div(h->k_stages, s) + 1850) + (s > 1 ? 2000 : 250);
-    const long long c2 = ceil_div(t2, h->num_sms / 2) * (460 * h->k_stages + 1900);
+    const long long c2 = ceil_div(t2, h->num_sms / 2) * (460 * h->k_stages + 1900 + (h->bias ? 500 : 0));
     if (c2 <= c1) {
       pl.pair = true;
       pl.bn = 256;
