@@ -102,7 +102,10 @@ extern "C" {
  *                  call (dqgemm_run) or given as codes
  *                  (dqgemm_run_fp8_block_quantized).  The products of a block
  *                  are summed in fp32 by the tensor core, scaled and summed
- *                  over the blocks in fp32.  K % 16 == 0, any N
+ *                  over the blocks in fp32.  The two scales are multiplied
+ *                  first: their product should be a normal fp32 number (below
+ *                  2^-126 it loses digits, above 2^128 it is infinite).
+ *                  K % 16 == 0, any N
  */
 typedef enum {
   DQ_INT4_G128 = 0,
@@ -330,7 +333,8 @@ typedef enum {
  *     r = x + residual,   v[m, k] = r[m, k] * w[k] / sqrt(mean_k r^2 + eps)
  * `residual` and `residual_out` ([M, K] of `type`) are both given or both
  * NULL; residual_out receives r rounded to `type`, and may be `residual` or
- * x (with ldx == K) itself.  The norm is of the unrounded sum.  `weight`: [K]
+ * x (with ldx == K) itself.  The norm is of the unrounded sum; its squares are
+ * summed in fp32 (|r| from 2^64 on overflows it).  `weight`: [K]
  * of weight_type, or NULL for ones.  eps >= 0.  A row is read once up to
  * K = 16384, twice beyond. */
 dqgemm_status dqgemm_rmsnorm(dqgemm_dtype type, const void* x, long long ldx, const void* residual,
@@ -408,7 +412,9 @@ dqgemm_status dqgemm_last_error(dqgemm_handle h);
  * waits of this handle's GEMM pipeline (0 restores the default, which is
  * DQGEMM_TIMEOUT_MS or 2 s).  A wait that does not complete at once gives up
  * when its limit has passed: the kernel then records DQ_ERR_TIMEOUT (read by
- * dqgemm_last_error) and writes no output of the tiles it gave up on.  The
+ * dqgemm_last_error) and writes no output of the tiles it gave up on
+ * (block-scaled handles: of the parts of a tile whose warps gave up; what is
+ * written is right).  The
  * waits for a CTA's own copies, tensor-core operations and received split-K
  * partials keep a limit of at least the default, so that no kernel leaves
  * memory that is still being written.  Calls already launched keep the limit
@@ -424,7 +430,7 @@ dqgemm_status dqgemm_selftest_timeout(int timeout_us, void* stream);
 
 /* Launch plan that dqgemm_run uses for a given M (for benchmarks and tests). */
 typedef struct {
-  int bn;               /* MMA N (activation rows per tile): 16, 32, 64 or 128 */
+  int bn;               /* activation rows per tile: 16, 32, 64, 128 or 256 */
   int m_tiles;          /* ceil(M / bn) */
   int n_tiles;          /* ceil(N / 128) (block-scaled with bn = 256: ceil(N / 256)) */
   int k_stages;         /* ceil(K / 128) */

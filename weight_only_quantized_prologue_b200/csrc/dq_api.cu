@@ -19,15 +19,15 @@ using namespace dq;
 
 namespace {
 
-// canonical storage sizes of dqgemm.h
-// the canonical storage of a W4A4 handle is that of its weight format
 // public format -> internal (-1: unknown)
 int internal_fmt(int fmt) {
   return fmt == DQ_FP8_BLOCK128 ? FMT_FP8B : fmt >= 0 && fmt <= FMT_W4A4NV ? fmt : -1;
 }
 
+// the canonical storage of a W4A4 handle is that of its weight format
 int storage_fmt(int fmt) { return fmt == FMT_W4A4MX ? FMT_MXFP4 : fmt == FMT_W4A4NV ? FMT_NVFP4 : fmt; }
 
+// canonical storage sizes of dqgemm.h
 size_t packed_bytes(int fmt, int K, int N) {
   fmt = storage_fmt(fmt);
   return is_4bit(fmt) ? (size_t)N * K / 2 : (size_t)N * K;

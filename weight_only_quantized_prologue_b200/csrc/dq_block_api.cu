@@ -77,8 +77,8 @@ int force_split() {
 //   4096 x 4096, from Python  8.4 / 11.6   8.5 / 11.7   9.6 / 11.7   9.7 / 11.7
 //   2048 x 2048, from Python  7.4 / 11.6   7.2 / 11.7   7.4 / 11.6   7.6 / 11.5
 // Experts, whose CTAs go through several tiles: 16 rows and at most 16 blocks a
-// CTA (7 x 1024 x 768: 6.2 us, on codes 5.0; but 64 x 4096 x 2048, 24 of 32
-// experts: 46 against 36).
+// CTA (7 rows, 5 of 8 of 1024 x 768: 6.0 / 6.3 us on the GPU; 16 rows, 12 of 32
+// of 4096 x 2048, 64 blocks a CTA: 26.6 / 24.4).
 bool quantizes(const dqgemm_s* h, int M) {
   if (!h->experts) return M <= 8;
   return M <= 16 && h->k_stages * ceil_div((long long)std::min(h->E, M) * h->n_tiles, h->num_sms) <= 16;
@@ -122,7 +122,7 @@ int cluster_capacity(dqgemm_s* h, int bn, int split) {
 
 // The split of K: the largest power of two S <= 8, S <= kb, whose T clusters of
 // S CTAs all run at once (1 x 2048 x 2048, T = 16: S = 8 would take two turns,
-// 10.1 us against 4.7 at S = 4).
+// 9.9 us against 4.6 at S = 4).
 int pick_split(dqgemm_s* h, long long T, int bn) {
   int s = 1;
   if (force_split() > 0) {

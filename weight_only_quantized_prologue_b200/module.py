@@ -10,8 +10,9 @@ Linear model"): ``calibrate_static_fp8`` records them.
 
 The op ``dqgemm::linear`` takes the layer's handle as an integer and has a
 fake (shape-only) implementation, so modules that use it can be traced; the
-real implementation is one ``dqgemm_run`` (or the quantize + FP8 GEMM pair of
-static FP8 from 128 rows on) on the current stream.  Nothing here computes:
+real implementation is one ``dqgemm_run`` (for static FP8 from 128 rows on the
+quantize + FP8 GEMM pair, for block-scaled FP8 one ``dqgemm_run_fp8_block``) on
+the current stream.  Nothing here computes:
 without ``libdqgemm.so`` the calls raise.
 """
 
