@@ -60,7 +60,8 @@ class Pair:
         self.abort = [False, False]
         self.filled = [0, 0]
         self.issued = [False, False]
-        self.flights = []                                   # in any order: landings of copies, signals
+        self.flights = []                                   # in any order: landings of copies, threads' arrivals
+        self.signals = [[[], []], [[], []]]                 # [half][cta]: commits' arrivals, in order
         self.mma = [[], []]                                 # in order, per half
         self.stage = [[None] * ST for _ in range(2)]        # [cta][stage]: block that is there
         self.reading = [[0] * ST for _ in range(2)]
@@ -151,9 +152,13 @@ class Pair:
     def engine(self):
         """One landing, signal or MMA step, if there is any."""
         kinds = [k for k in (0, 1) if self.mma[k]] + (["f"] if self.flights else [])
+        kinds += [q for h in self.signals for q in h if q]
         if not kinds:
             return False
         k = self.rng.choice(kinds)
+        if isinstance(k, list):
+            k.pop(0)()
+            return True
         if k == "f":
             self.flights.pop(self.rng.randrange(len(self.flights)))[1]()
             return True
@@ -164,7 +169,7 @@ class Pair:
                 self.partial[c][k][arg % PB] = (arg, set())
         else:
             for c, b in enumerate(arg):
-                self.flights.append((c, b.arrive))
+                self.signals[k][c].append(b.arrive)
         return True
 
     def run(self, agents):
@@ -183,18 +188,20 @@ class Pair:
                 idle = 0
             assert idle < 20000 or self.engine(), "a wait that never ends"
 
-    def end(self, cta):
-        """What a CTA does between the two cluster barriers where a wait gave up."""
-        for i in range(self.filled[cta], self.filled[1 - cta]):
-            self.flights.append((0, self.full[i % ST].arrive))
-        last = max(self.filled)
-        if cta == 0:
-            for i in range(max(0, last - ST), last):
-                yield from self.sure_wait(self.full[i % ST], (i // ST) % 2)
-        else:
+    def end(self, cta, gave_up):
+        """What a CTA does behind the first cluster barrier."""
+        if gave_up:
+            for i in range(self.filled[cta], self.filled[1 - cta]):
+                self.flights.append((0, self.full[i % ST].arrive))
+            last = max(self.filled)
+            if cta == 0:
+                for i in range(max(0, last - ST), last):
+                    yield from self.sure_wait(self.full[i % ST], (i // ST) % 2)
+        if cta == 1:
             for h in range(2):
                 if self.issued[h]:
                     yield from self.sure_wait(self.drain[1][h], 0)
+        assert gave_up or not any(h[cta] for h in self.signals), "a CTA leaves before its signals have arrived"
 
 
 @pytest.mark.parametrize("quit_rate", [0.0, 0.0002, 0.002, 0.02, 0.3])
@@ -207,11 +214,11 @@ def test_copies_sums_and_ends(blocks, quit_rate):
               [p.epilogue(c, h, w) for c in range(2) for h in range(2) for w in range(4)])
         # the first cluster barrier
         assert abs(p.filled[0] - p.filled[1]) <= ST
-        if any(p.abort):
-            gave_up += 1
-            p.run([p.end(c) for c in range(2)])
-            assert not any(k == "mma" for q in p.mma for k, _ in q)
-        else:
+        gave_up += any(p.abort)
+        p.run([p.end(c, any(p.abort)) for c in range(2)])
+        assert not any(k == "mma" for q in p.mma for k, _ in q)
+        assert not any(q for h in p.signals for q in h), "a CTA leaves before its signals have arrived"
+        if not any(p.abort):
             assert p.filled == [blocks, blocks]
             assert all(p.summed.get((c, h, w), 0) == blocks for c in range(2) for h in range(2) for w in range(4))
             assert not p.mma[0] and not p.mma[1]

@@ -1128,25 +1128,24 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
   // an epilogue warp)
   cluster_sync();
   const uint32_t mine = *ended, other = *other_ended;
-  if ((mine | other) & 1u) {
-    // A wait gave up.  Copies and MMAs of either CTA may still run: they end
-    // before this CTA's shared memory is given back.  A CTA has filled at
-    // most ST stages more than the other; for those the other arrives too, with
-    // no bytes, so that each phase the leader waits for here completes.
-    if (warp == 0 && elect_one()) {
+  const bool gave_up = (mine | other) & 1u;
+  if (warp == 0 && elect_one()) {
+    if (gave_up) {
+      // Copies and MMAs of either CTA may still run: they end before this CTA's
+      // shared memory is given back.  A CTA has filled at most ST stages more
+      // than the other; for those the other arrives too, with no bytes, so
+      // that each phase the leader waits for here completes.
       const int a = (int)(mine >> 3), b = (int)(other >> 3), last = max(a, b);
       for (int i = a; i < b; ++i) mbar_arrive_cluster(dsmem_addr(full, 0) + (i % C::ST) * 8);
-      if (rank == 0) {
-        for (int i = last > C::ST ? last - C::ST : 0; i < last; ++i)
-          block_wait_pair<true>(&full[i % C::ST], (i / C::ST) & 1, ctl_drain());
-      } else {
-        for (int h = 0; h < 2; ++h)
-          if (other >> (1 + h) & 1u) block_wait_pair<true>(drain + h, 0, ctl_drain());
-      }
+      for (int i = last > C::ST ? last - C::ST : 0; rank == 0 && i < last; ++i)
+        block_wait_pair<true>(&full[i % C::ST], (i / C::ST) & 1, ctl_drain());
     }
-    __syncwarp();
-    cluster_sync();
+    // the leader's last signal of each half (the leader has waited for its own)
+    for (int h = 0; rank == 1 && h < 2; ++h)
+      if (other >> (1 + h) & 1u) block_wait_pair<true>(drain + h, 0, ctl_drain());
   }
+  __syncwarp();
+  if (gave_up) cluster_sync();
   tc_fence_after();
   if (warp == 0) tmem_dealloc_pair(tmem, C::TMEM_COLS);
 }
